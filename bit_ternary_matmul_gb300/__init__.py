@@ -37,6 +37,12 @@ Q2_0_NOALLOC_SCRATCH_BYTES = 1 << 20
 Q2_0_PREC_F16_SPLIT = 0
 Q2_0_PREC_F16 = 1
 
+Q2_0_TYPE_F16 = 0
+Q2_0_TYPE_BF16 = 1
+
+Q2_0_ROPE_HALVES = 0
+Q2_0_ROPE_PAIRS = 1
+
 Q2_0_DEVERR_NONE = 0
 Q2_0_DEVERR_BAD_ID = 1
 Q2_0_DEVERR_TIMEOUT = 2
@@ -57,6 +63,9 @@ EXPORTS = (
     "q2_0_split_bytes", "q2_0_split_layout", "q2_0_join_layout", "q2_0_mul_mat_vec_split",
     "q2_0_mm_plan_create", "q2_0_mm_plan_execute", "q2_0_mm_plan_launches",
     "q2_0_mm_plan_destroy",
+    "q2_0_kv_append", "q2_0_attn_plan_create", "q2_0_attn_plan_execute",
+    "q2_0_attn_plan_launches", "q2_0_attn_plan_destroy",
+    "q2_0_beam_select_workspace_size", "q2_0_beam_select", "q2_0_beam_reorder",
 )
 
 
@@ -74,6 +83,20 @@ class _MvDesc(ctypes.Structure):
 class _MmDesc(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("M", ctypes.c_int64)]
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("n_layers", ctypes.c_int), ("n_kv", ctypes.c_int), ("page", ctypes.c_int),
+                ("dim", ctypes.c_int), ("type", ctypes.c_int)]
+
+
+class _AttnDesc(ctypes.Structure):
+    _fields_ = [("cache", _KvCacheStruct), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("n_groups", ctypes.c_int64), ("n_seq", ctypes.c_int64), ("n_q", ctypes.c_int),
+                ("scale", ctypes.c_float), ("prefix_table", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("prefix_width", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("width", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -160,6 +183,24 @@ def lib():
             L.q2_0_mul_mat_vec_split.restype = i32
             L.q2_0_quantize_ref.argtypes = [vp, vp, i64, i64, vp]
             L.q2_0_quantize_ref.restype = i32
+            L.q2_0_kv_append.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64, i64, i32, vp, vp, vp,
+                                         vp, i64, i64, vp, i64, i32, i32, vp, vp]
+            L.q2_0_kv_append.restype = i32
+            L.q2_0_attn_plan_create.argtypes = [ctypes.POINTER(_AttnDesc), ctypes.POINTER(vp)]
+            L.q2_0_attn_plan_create.restype = i32
+            L.q2_0_attn_plan_execute.argtypes = [vp, i32, vp]
+            L.q2_0_attn_plan_execute.restype = i32
+            L.q2_0_attn_plan_launches.argtypes = [vp]
+            L.q2_0_attn_plan_launches.restype = i32
+            L.q2_0_attn_plan_destroy.argtypes = [vp]
+            L.q2_0_attn_plan_destroy.restype = None
+            L.q2_0_beam_select_workspace_size.argtypes = [i64, i32, i64, i32]
+            L.q2_0_beam_select_workspace_size.restype = sz
+            L.q2_0_beam_select.argtypes = [vp, i64, vp, vp, i32, i64, i32, i64, i32, vp, vp, vp, vp,
+                                           sz, vp]
+            L.q2_0_beam_select.restype = i32
+            L.q2_0_beam_reorder.argtypes = [vp, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp]
+            L.q2_0_beam_reorder.restype = i32
             L.q2_0_get_error.argtypes = [vp, ctypes.POINTER(i64)]
             L.q2_0_get_error.restype = i32
             _lib = L
@@ -490,6 +531,220 @@ def q2_0_quantize_ref(src: torch.Tensor, nrows: int, K: int, dst: torch.Tensor |
                                  _stream(stream))
     _check("q2_0_quantize_ref", st)
     return dst
+
+
+# ---- decode step on a paged key/value cache --------------------------------------
+_CACHE_TYPES = {torch.float16: Q2_0_TYPE_F16, torch.bfloat16: Q2_0_TYPE_BF16}
+
+
+def _rows(t: torch.Tensor, name: str, n_tokens: int, heads: int, dim: int):
+    """(data_ptr, floats from a token to the next) of f32 [n_tokens][heads][dim] (or
+    [n_tokens][heads * dim]) whose tokens are contiguous but may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == dim and stride[2] == 1 and \
+            (stride[1] == dim or heads == 1)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
+    if not ok or shape[0] != n_tokens:
+        raise ValueError(f"{name} must be [{n_tokens}][{heads}][{dim}] with contiguous tokens")
+    return t.data_ptr(), stride[0] if n_tokens > 1 else heads * dim
+
+
+class KvCache:
+    """A paged key/value cache (q2_0_kv_cache): keeps references to its tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        """k, v: f16 or bf16 [n_layers][n_pages][n_kv][page][dim], contiguous."""
+        if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
+            raise TypeError("k and v must be torch.Tensors")
+        if k.dtype not in _CACHE_TYPES:
+            raise ValueError(f"k must be torch.float16 or torch.bfloat16, got {k.dtype}")
+        if k.dim() != 5 or v.shape != k.shape:
+            raise ValueError("k and v must both be [n_layers][n_pages][n_kv][page][dim]")
+        if v.device != k.device:
+            raise ValueError("k and v must be on one device")
+        self.k, self.v = k, v
+        self.n_layers, self.n_pages, self.n_kv, self.page, self.dim = k.shape
+        self._c = _KvCacheStruct(_dev(k, "k", k.dtype), _dev(v, "v", k.dtype), self.n_pages,
+                                 self.n_layers, self.n_kv, self.page, self.dim,
+                                 _CACHE_TYPES[k.dtype])
+        self._ref = ctypes.addressof(self._c)
+
+
+def q2_0_kv_append(cache: KvCache, layer: int, q: torch.Tensor | None, k: torch.Tensor,
+                   v: torch.Tensor, pos: torch.Tensor | None, slot: torch.Tensor,
+                   table: torch.Tensor, rope: torch.Tensor | None, style: int = Q2_0_ROPE_HALVES,
+                   seq: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor | None:
+    """Rotates q and k, stores k and v in the cache's pages; returns the rotated q.
+
+    q f32 [n_tokens][n_q][dim] (or None), k and v f32 [n_tokens][n_kv][dim]: tokens may lie
+    apart, as slices of one product's rows do; pos, slot, seq int32 [n_tokens] (seq None:
+    token t belongs to row t of the table); table int32 [n_seq][width]; rope f32
+    [n_pos][rot], cosines then sines (None: no rotation); q_out [n_tokens][n_q][dim] in the
+    cache's type.
+    """
+    T = k.shape[0]
+    qp, qs, n_q, qo = None, 0, 0, None
+    if q is not None:
+        n_q = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
+        qp, qs = _rows(q, "q", T, n_q, cache.dim)
+        if q_out is None:
+            q_out = torch.empty((T, n_q, cache.dim), dtype=cache.k.dtype, device=q.device)
+        qo = _dev(q_out, "q_out", cache.k.dtype, T * n_q * cache.dim)
+    kp, ks = _rows(k, "k", T, cache.n_kv, cache.dim)
+    vp, vs = _rows(v, "v", T, cache.n_kv, cache.dim)
+    if table.dim() != 2:
+        raise ValueError("table must be [n_seq][width]")
+    n_pos, rot = (0, 0) if rope is None else rope.shape
+    st = lib().q2_0_kv_append(
+        cache._ref, layer, qp, qs, kp, ks, vp, vs, T, n_q,
+        None if pos is None else _dev(pos, "pos", torch.int32, T),
+        _dev(slot, "slot", torch.int32, T),
+        None if seq is None else _dev(seq, "seq", torch.int32, T),
+        _dev(table, "table", torch.int32), table.shape[0], table.shape[1],
+        None if rope is None else _dev(rope, "rope", torch.float32), n_pos, rot, style, qo,
+        _stream(stream))
+    _check("q2_0_kv_append", st)
+    return q_out
+
+
+class AttnPlan:
+    """Decode attention with shared prefixes (q2_0_attn_plan_*): keeps references to its tensors."""
+
+    def __init__(self, cache: KvCache, q: torch.Tensor, out: torch.Tensor, table: torch.Tensor,
+                 length: torch.Tensor, prefix_table: torch.Tensor | None = None,
+                 prefix_len: torch.Tensor | None = None, scale: float | None = None):
+        """q, out [n_groups * n_seq][n_q][dim] in the cache's type; table int32 [n_groups * n_seq]
+        [width], length int32 [n_groups * n_seq]; prefix_table int32 [n_groups][prefix_width],
+        prefix_len int32 [n_groups] (None: nothing is shared). scale: 1 / sqrt(dim) if None."""
+        if q.dim() != 3 or q.shape[2] != cache.dim or out.shape != q.shape:
+            raise ValueError("q and out must be [n_groups * n_seq][n_q][dim]")
+        n, n_q = q.shape[0], q.shape[1]
+        if table.dim() != 2 or table.shape[0] != n:
+            raise ValueError("table must be [n_groups * n_seq][width]")
+        groups, pw, pt, pl = 1, 0, None, None
+        if prefix_table is not None:
+            if prefix_table.dim() != 2 or prefix_table.shape[0] < 1 or n % prefix_table.shape[0]:
+                raise ValueError("prefix_table must be [n_groups][prefix_width]")
+            groups, pw = prefix_table.shape
+            pt = _dev(prefix_table, "prefix_table", torch.int32)
+            if prefix_len is None:
+                raise ValueError("prefix_len is needed with prefix_table")
+            pl = _dev(prefix_len, "prefix_len", torch.int32, groups)
+        d = _AttnDesc(cache._c, _dev(q, "q", cache.k.dtype), _dev(out, "out", cache.k.dtype), groups,
+                      n // groups, n_q, cache.dim ** -0.5 if scale is None else scale, pt, pl, pw,
+                      _dev(table, "table", torch.int32), _dev(length, "length", torch.int32, n),
+                      table.shape[1])
+        self._keep = (cache, q, out, table, length, prefix_table, prefix_len)
+        h = ctypes.c_void_p()
+        _check("q2_0_attn_plan_create", lib().q2_0_attn_plan_create(ctypes.byref(d), ctypes.byref(h)))
+        self._h = h
+        self.out = out
+
+    @property
+    def launches(self) -> int:
+        return int(lib().q2_0_attn_plan_launches(self._h))
+
+    def execute(self, layer: int = 0, stream=None) -> torch.Tensor:
+        _check("q2_0_attn_plan_execute",
+               lib().q2_0_attn_plan_execute(self._h, layer, _stream(stream)))
+        return self.out
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().q2_0_attn_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def q2_0_beam_select_workspace_size(n_groups: int, n_beams: int, n_vocab: int, n_out: int) -> int:
+    return int(lib().q2_0_beam_select_workspace_size(n_groups, n_beams, n_vocab, n_out))
+
+
+def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | None = None,
+                     done: torch.Tensor | None = None, done_token: int = 0,
+                     out: tuple | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> tuple:
+    """(scores, parent, token) [n_groups][n_out] of the best continuations of each group's beams.
+
+    logits f32 [n_groups][n_beams][n_vocab]: rows contiguous, evenly apart; scores f32 and done
+    uint8 or bool [n_groups][n_beams]. n_out: n_beams if None. out: three tensors to write to
+    (f32, int32, int32).
+    """
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype != torch.float32:
+        raise ValueError(f"logits must be {torch.float32}, got {logits.dtype}")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [n_groups][n_beams][n_vocab]")
+    G, W, V = logits.shape
+    gs, stride, one = logits.stride()
+    if W == 1:
+        stride = gs if G > 1 else V
+    if (V > 1 and one != 1) or (G > 1 and gs != W * stride):
+        raise ValueError("logits must have contiguous rows, evenly apart")
+    n_out = W if n_out is None else n_out
+    if out is None:
+        out = (torch.empty((G, n_out), dtype=torch.float32, device=logits.device),
+               torch.empty((G, n_out), dtype=torch.int32, device=logits.device),
+               torch.empty((G, n_out), dtype=torch.int32, device=logits.device))
+    dp = None
+    if done is not None:
+        dp = _dev(done, "done", torch.bool if done.dtype == torch.bool else torch.uint8, G * W)
+    wp, wb = None, 0
+    if workspace is not None:
+        wb = workspace.numel()
+        wp = _dev(workspace, "workspace", torch.uint8,
+                  q2_0_beam_select_workspace_size(G, W, V, n_out))
+    st = lib().q2_0_beam_select(logits.data_ptr(), stride, _dev(scores, "scores", torch.float32, G * W),
+                                dp, done_token, G, W, V, n_out,
+                                _dev(out[0], "out[0]", torch.float32, G * n_out),
+                                _dev(out[1], "out[1]", torch.int32, G * n_out),
+                                _dev(out[2], "out[2]", torch.int32, G * n_out), wp, wb,
+                                _stream(stream))
+    _check("q2_0_beam_select", st)
+    return out
+
+
+def q2_0_beam_reorder(cache: KvCache, parent: torch.Tensor, table: torch.Tensor,
+                      length: torch.Tensor, fresh: torch.Tensor, out: tuple | None = None,
+                      stream=None) -> tuple:
+    """(table, length, used) after the beams went on from their parents.
+
+    parent int32 [n_groups][n_beams]; table int32 [n_groups * n_beams][width]; length, fresh
+    int32 [n_groups * n_beams]. out: three int32 tensors to write to.
+    """
+    if parent.dim() != 2 or table.dim() != 2 or table.shape[0] != parent.numel():
+        raise ValueError("parent must be [n_groups][n_beams], table [n_groups * n_beams][width]")
+    G, W = parent.shape
+    n, width = table.shape
+    if out is None:
+        out = (torch.empty_like(table), torch.empty_like(length),
+               torch.empty(n, dtype=torch.int32, device=table.device))
+    st = lib().q2_0_beam_reorder(cache._ref, _dev(parent, "parent", torch.int32), G, W,
+                                 _dev(table, "table", torch.int32),
+                                 _dev(length, "length", torch.int32, n), width,
+                                 _dev(fresh, "fresh", torch.int32, n),
+                                 _dev(out[0], "out[0]", torch.int32, n * width),
+                                 _dev(out[1], "out[1]", torch.int32, n),
+                                 _dev(out[2], "out[2]", torch.int32, n), _stream(stream))
+    _check("q2_0_beam_reorder", st)
+    return out
 
 
 def q2_0_test_inject_stall(stage: int, wait_limit_ns: int) -> None:

@@ -1,5 +1,7 @@
 // C-ABI entry points of libq2_0: argument validation, device checks, scratch
 // handling and the device error word. Kernels live in the other .cu files.
+#include <math.h>
+
 #include <mutex>
 
 #include "q2_0_device.cuh"
@@ -377,6 +379,131 @@ int q2_0_quantize_ref(const float *src, void *dst, int64_t nrows, int64_t K, voi
     if (st != Q2_0_OK) return st;
     return cuda_status(launch_quantize(src, static_cast<uint8_t *>(dst), nrows, K,
                                        as_stream(stream)));
+}
+
+// A cache struct a call may use: shapes, types, alignment, and rows of `dim`
+// elements that a 32-bit tensor-map coordinate reaches.
+static bool valid_cache(const q2_0_kv_cache *c) {
+    if (!c || !c->k || !c->v || c->n_pages < 1 || c->n_layers < 1 || c->n_kv < 1) return false;
+    if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15u) return false;
+    if (c->dim != 64 && c->dim != 128) return false;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return false;
+    if (c->type != Q2_0_TYPE_F16 && c->type != Q2_0_TYPE_BF16) return false;
+    const int64_t most = (int64_t(1) << 31) - 1;
+    return c->n_pages <= most && c->n_kv <= most / c->page &&
+           c->n_layers <= most / (int64_t(c->n_kv) * c->page) &&
+           c->n_pages <= most / (int64_t(c->n_layers) * c->n_kv * c->page);
+}
+
+int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_t q_stride,
+                   const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                   int64_t n_tokens, int n_q, const int32_t *pos, const int32_t *slot,
+                   const int32_t *seq, const int32_t *table, int64_t n_seq, int64_t width,
+                   const float *rope, int64_t n_pos, int rot, int style, void *q_out,
+                   void *stream) {
+    if (!valid_cache(cache) || layer < 0 || layer >= cache->n_layers || n_tokens < 0 ||
+        n_tokens > (int64_t(1) << 31) - 1 || n_q < 0 || n_q > (1 << 16) || cache->n_kv > (1 << 16) ||
+        rot < 0 || rot > cache->dim || rot % 2 ||
+        (style != Q2_0_ROPE_HALVES && style != Q2_0_ROPE_PAIRS))
+        return Q2_0_EINVAL;
+    if (n_tokens == 0) return Q2_0_OK;
+    if (!k || !v || !slot || !table || n_seq < 1 || width < 1 || (!seq && n_tokens > n_seq) ||
+        (n_q && (!q || !q_out || q_stride < int64_t(n_q) * cache->dim)) ||
+        k_stride < int64_t(cache->n_kv) * cache->dim ||
+        v_stride < int64_t(cache->n_kv) * cache->dim || (rot && (!rope || !pos || n_pos < 1)))
+        return Q2_0_EINVAL;
+    int st = check_device(nullptr);
+    if (st != Q2_0_OK) return st;
+    unsigned long long *err = error_word_ptr();
+    if (!err) return Q2_0_ECUDA;
+    return cuda_status(launch_append(*cache, layer, q, q_stride, k, k_stride, v, v_stride, n_tokens,
+                                     n_q, pos, slot, seq, table, n_seq, width, rope, n_pos, rot,
+                                     style, q_out, err, as_stream(stream)));
+}
+
+int q2_0_attn_plan_create(const q2_0_attn_desc *d, q2_0_attn_plan **plan) {
+    if (!plan) return Q2_0_EINVAL;
+    *plan = nullptr;
+    if (!d || !valid_cache(&d->cache) || !d->q || !d->out || !d->table || !d->len ||
+        ((reinterpret_cast<uintptr_t>(d->q) | reinterpret_cast<uintptr_t>(d->out)) & 15u) ||
+        d->n_groups < 1 || d->n_seq < 1 || d->n_groups > 65535 || d->n_seq > 65535 ||
+        d->n_groups * d->n_seq > 65535 || d->n_q < 1 || d->n_q > 65535 ||
+        d->n_q % d->cache.n_kv || d->n_q / d->cache.n_kv > 64 || d->width < 1 ||
+        d->prefix_width < 0 || (d->prefix_width && (!d->prefix_table || !d->prefix_len)) ||
+        !(d->scale > -INFINITY && d->scale < INFINITY))
+        return Q2_0_EINVAL;
+    // a sequence's tokens are counted in 32 bits
+    const int64_t most = ((int64_t(1) << 31) - 1) / d->cache.page - 1;
+    if (d->width > most || d->prefix_width > most) return Q2_0_EINVAL;
+    int st = check_device(nullptr);
+    if (st != Q2_0_OK) return st;
+    return attn_plan_create(*d, plan);
+}
+
+int q2_0_attn_plan_execute(const q2_0_attn_plan *plan, int layer, void *stream) {
+    if (!plan || layer < 0 || layer >= attn_plan_layers(plan)) return Q2_0_EINVAL;
+    return attn_plan_execute(plan, layer, as_stream(stream));
+}
+
+int q2_0_attn_plan_launches(const q2_0_attn_plan *plan) {
+    return plan ? attn_plan_launches(plan) : 0;
+}
+
+void q2_0_attn_plan_destroy(q2_0_attn_plan *plan) {
+    if (plan) attn_plan_destroy(plan);
+}
+
+static bool valid_select(int64_t n_groups, int n_beams, int64_t n_vocab, int n_out) {
+    return n_groups >= 0 && n_beams >= 1 && n_beams <= 64 && n_groups <= 65535 / n_beams &&
+           n_vocab >= 1 && n_vocab < (int64_t(1) << 31) - (1 << 16) && n_out >= 1 && n_out <= 32;
+}
+
+size_t q2_0_beam_select_workspace_size(int64_t n_groups, int n_beams, int64_t n_vocab, int n_out) {
+    if (!valid_select(n_groups, n_beams, n_vocab, n_out)) return 0;
+    return select_workspace_bytes(n_groups, n_beams, n_vocab, n_out);
+}
+
+int q2_0_beam_select(const float *logits, int64_t stride, const float *score, const uint8_t *done,
+                     int done_token, int64_t n_groups, int n_beams, int64_t n_vocab, int n_out,
+                     float *score_out, int32_t *parent, int32_t *token, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    if (!valid_select(n_groups, n_beams, n_vocab, n_out) || stride < n_vocab) return Q2_0_EINVAL;
+    if (n_groups == 0) return Q2_0_OK;
+    if (!logits || !score || !score_out || !parent || !token) return Q2_0_EINVAL;
+    const size_t need = select_workspace_bytes(n_groups, n_beams, n_vocab, n_out);
+    if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return Q2_0_EINVAL;
+    int st = check_device(nullptr);
+    if (st != Q2_0_OK) return st;
+    const SelectArgs a = {logits,  stride,  score, done,      done_token, n_groups,
+                          n_vocab, n_beams, n_out, score_out, parent,     token};
+    if (workspace) return cuda_status(select_run(a, workspace, as_stream(stream)));
+    PoolScratch ws;
+    st = ws.alloc(need, as_stream(stream));
+    if (st != Q2_0_OK) return st;
+    st = cuda_status(select_run(a, ws.ptr, as_stream(stream)));
+    int st2 = ws.release();
+    return st != Q2_0_OK ? st : st2;
+}
+
+int q2_0_beam_reorder(const q2_0_kv_cache *cache, const int32_t *parent, int64_t n_groups,
+                      int n_beams, const int32_t *table, const int32_t *len, int64_t width,
+                      const int32_t *fresh, int32_t *table_out, int32_t *len_out, int32_t *used,
+                      void *stream) {
+    if (!valid_cache(cache) || n_groups < 0 || n_beams < 1 || n_beams > 1024 || width < 1 ||
+        width > ((int64_t(1) << 31) - 1) / cache->page || cache->n_layers > 65535 ||
+        n_groups > ((int64_t(1) << 31) - 1) / n_beams)
+        return Q2_0_EINVAL;
+    if (n_groups == 0) return Q2_0_OK;
+    if (!parent || !table || !len || !fresh || !table_out || !len_out || !used) return Q2_0_EINVAL;
+    int st = check_device(nullptr);
+    if (st != Q2_0_OK) return st;
+    unsigned long long *err = error_word_ptr();
+    if (!err) return Q2_0_ECUDA;
+    const ReorderArgs a = {cache->k, cache->v, cache->n_pages, cache->n_kv, log2_of(cache->page),
+                           cache->dim, parent, table, len, fresh, table_out, len_out, used, width,
+                           n_beams, err};
+    return cuda_status(launch_reorder(a, n_groups * n_beams, cache->n_layers, as_stream(stream)));
 }
 
 int q2_0_get_error(void *stream, int64_t *info) {

@@ -94,4 +94,47 @@ int mm_plan_execute(const q2_0_mm_plan *plan, cudaStream_t s);
 int mm_plan_launches(const q2_0_mm_plan *plan);
 void mm_plan_destroy(q2_0_mm_plan *plan);
 
+// paged key/value cache (kv_cache.cu)
+int log2_of(int page);
+cudaError_t launch_append(const q2_0_kv_cache &c, int layer, const float *q, int64_t q_stride,
+                          const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                          int64_t n_tokens, int n_q, const int32_t *pos, const int32_t *slot,
+                          const int32_t *seq, const int32_t *table, int64_t n_seq, int64_t width,
+                          const float *rope, int64_t n_pos, int rot, int style, void *q_out,
+                          unsigned long long *err, cudaStream_t s);
+
+struct ReorderArgs {
+    void *k, *v;
+    int64_t n_pages;
+    int n_kv, page_shift, dim;
+    const int32_t *parent, *table, *len, *fresh;
+    int32_t *table_out, *len_out, *used;
+    int64_t width;
+    int n_beams;
+    unsigned long long *err;
+};
+cudaError_t launch_reorder(const ReorderArgs &a, int64_t n, int n_layers, cudaStream_t s);
+
+// attention plans (attn.cu; opaque to the C ABI)
+int attn_plan_create(const q2_0_attn_desc &desc, q2_0_attn_plan **plan);
+int attn_plan_execute(const q2_0_attn_plan *plan, int layer, cudaStream_t s);
+int attn_plan_launches(const q2_0_attn_plan *plan);
+int attn_plan_layers(const q2_0_attn_plan *plan);
+void attn_plan_destroy(q2_0_attn_plan *plan);
+
+// beam selection (beam.cu)
+struct SelectArgs {
+    const float *logits;
+    int64_t stride;
+    const float *score;
+    const uint8_t *done;
+    int done_token;
+    int64_t n_groups, n_vocab;
+    int n_beams, n_out;
+    float *score_out;
+    int32_t *parent, *token;
+};
+size_t select_workspace_bytes(int64_t n_groups, int n_beams, int64_t n_vocab, int n_out);
+cudaError_t select_run(const SelectArgs &a, void *ws, cudaStream_t s);
+
 }  // namespace q2

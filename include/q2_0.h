@@ -56,7 +56,7 @@ typedef enum q2_0_status {
 
 /* Device error codes (first error wins until cleared). */
 #define Q2_0_DEVERR_NONE 0
-#define Q2_0_DEVERR_BAD_ID 1  /* get_rows / mul_mat_id: ids[info] out of range */
+#define Q2_0_DEVERR_BAD_ID 1  /* get_rows / mul_mat_id: ids[info] out of range; cache calls: see there */
 #define Q2_0_DEVERR_TIMEOUT 2 /* a pipeline wait gave up; info = kernel tag */
 
 /* GEMM activation precision. F32 activations are used by the tensor cores as
@@ -369,6 +369,181 @@ int q2_0_g128_mul_mat_vec(const void *w, const float *x, float *y, int64_t N, in
  * decisions use the unrounded amax); amax == 0 gives d = 0 and code 1.
  */
 int q2_0_quantize_ref(const float *src, void *dst, int64_t nrows, int64_t K, void *stream);
+
+/* ---- decode step on a paged key/value cache ---------------------------------
+ * The operators between a decoder's products: rotated keys and values appended
+ * to a paged cache, attention of sequences that share a prefix, and a beam
+ * search's selection and reordering on the same pages. (The Q2_0 pages have no
+ * counterpart; these calls take the F32 outputs of the mat-vec and GEMM calls
+ * and give F16 or BF16 activations.)
+ */
+
+/* Element type of a cache and of the activations that go with it. */
+typedef enum q2_0_type { Q2_0_TYPE_F16 = 0, Q2_0_TYPE_BF16 = 1 } q2_0_type;
+
+/* Which elements of a head a position turns together, rot of them in all:
+ * HALVES (i, i + rot/2), PAIRS (2i, 2i + 1), i < rot/2. Elements from rot on
+ * are left as they are. */
+typedef enum q2_0_rope { Q2_0_ROPE_HALVES = 0, Q2_0_ROPE_PAIRS = 1 } q2_0_rope;
+
+/*
+ * A paged key/value cache: two device arrays of the same layout,
+ * [n_layers][n_pages][n_kv][page][dim], owned by the caller. A page holds
+ * `page` tokens of every kv head of one layer; a sequence's tokens lie in the
+ * pages that its row of a page table names, token t in page table[t / page] at
+ * place t % page (the same page ids in every layer). The struct is read during
+ * the call (or plan_create) it is given to and not kept.
+ *   k, v 16-byte aligned; dim 64 or 128; page 16, 32, 64, 128 or 256; type a
+ *   q2_0_type; n_layers * n_pages * n_kv * page < 2^31 (byte offsets are 64-bit).
+ */
+typedef struct q2_0_kv_cache {
+    void *k;
+    void *v;
+    int64_t n_pages;
+    int n_layers;
+    int n_kv;
+    int page;
+    int dim;
+    int type;
+} q2_0_kv_cache;
+
+/*
+ * q2_0_kv_append — rotates q and k by their tokens' positions, and stores k and
+ * v in one layer of the cache.
+ *   q, k, v   F32, token t's heads [n_q or n_kv][dim] at q + t * q_stride (strides
+ *             in floats, >= heads * dim; so the three may be slices of one
+ *             product's rows). q and q_out may be NULL with n_q = 0.
+ *   pos       int32 [n_tokens], the row of `rope` that turns the token.
+ *   slot      int32 [n_tokens], the token's place in its sequence's row of
+ *             `table`; a negative slot stores nothing (padding), q is still
+ *             written.
+ *   seq       int32 [n_tokens], the row of `table` [n_seq][width] of the
+ *             token's sequence; NULL: token t belongs to row t (n_tokens <= n_seq).
+ *   rope      F32 [n_pos][rot]: the cosines of the rot/2 angles of a position,
+ *             then their sines. rot even, 0..dim; rot = 0: nothing turns, and
+ *             rope and pos may be NULL.
+ *   q_out     [n_tokens][n_q][dim] in the cache's type.
+ * (a, b) -> (a c - b s, a s + b c) in f32, each rounded once to the cache's
+ * type. No two tokens of a call may name the same place. A position, sequence,
+ * table column or page id that is out of range stores nothing of its token
+ * (q_out, k and v stay unwritten) and records Q2_0_DEVERR_BAD_ID with info = t.
+ * n_tokens == 0 is a no-op.
+ */
+int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_t q_stride,
+                   const float *k, int64_t k_stride, const float *v, int64_t v_stride,
+                   int64_t n_tokens, int n_q, const int32_t *pos, const int32_t *slot,
+                   const int32_t *seq, const int32_t *table, int64_t n_seq, int64_t width,
+                   const float *rope, int64_t n_pos, int rot, int style, void *q_out,
+                   void *stream);
+
+/*
+ * Decode attention of n_groups * n_seq sequences, one query token each, over a
+ * paged cache. The sequences of a group (b / n_seq) share a prefix, whose keys
+ * and values are read once for all of them; each goes on with tokens of its own:
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . k_t) v_t, t over the first
+ *   prefix_len[b / n_seq] tokens of the group's prefix_table row, then over the
+ *   first len[b] tokens of b's table row; query head h reads kv head
+ *   h / (n_q / n_kv). Where both lengths are 0 the output is 0. A prefix need
+ *   not end with a page: the places past a length are never used, whatever
+ *   they hold.
+ *   q, out    [n_groups * n_seq][n_q][dim] in the cache's type, 16-byte aligned;
+ *             n_q a multiple of n_kv, n_q / n_kv <= 64; n_groups * n_seq <= 65535.
+ *   prefix_table int32 [n_groups][prefix_width], prefix_len int32 [n_groups]:
+ *             both NULL with prefix_width = 0 where nothing is shared.
+ *   table     int32 [n_groups * n_seq][width], len int32 [n_groups * n_seq].
+ *   Tables and lengths are read at each execute: a decode loop updates them on
+ *   the device, and one captured execute serves all its steps.
+ * Precision: scores, softmax sums and output sums are f32; each weight
+ * exp(score - reference) enters its product with v rounded to the cache's type
+ * (2^-11 or 2^-8 of itself), and so is the output: it
+ * is within u (sum p|v| + |out|) and f32 rounding of the exact one, u that
+ * rounding and p the softmax weights.
+ * A length outside [0, width * page] is taken as the nearer bound, and a page
+ * id outside [0, n_pages) as page 0; both record Q2_0_DEVERR_BAD_ID with info =
+ * the sequence (or n_groups * n_seq + the group).
+ * q2_0_attn_plan_create keeps the pointers, encodes the TMA descriptors and
+ * allocates the plan's scratch; q2_0_attn_plan_execute runs one layer on
+ * `stream`, allocates nothing and may be captured in a CUDA graph. The plan
+ * belongs to the device current at creation; executes of one plan must not
+ * overlap on the GPU (they share its scratch). Destroy it after the last
+ * execute has completed.
+ */
+typedef struct q2_0_attn_desc {
+    q2_0_kv_cache cache;
+    const void *q;
+    void *out;
+    int64_t n_groups;
+    int64_t n_seq; /* sequences of a group */
+    int n_q;
+    float scale;
+    const int32_t *prefix_table;
+    const int32_t *prefix_len;
+    int64_t prefix_width;
+    const int32_t *table;
+    const int32_t *len;
+    int64_t width;
+} q2_0_attn_desc;
+
+typedef struct q2_0_attn_plan q2_0_attn_plan;
+
+int q2_0_attn_plan_create(const q2_0_attn_desc *desc, q2_0_attn_plan **plan);
+int q2_0_attn_plan_execute(const q2_0_attn_plan *plan, int layer, void *stream);
+/* Number of kernel launches one execute performs. */
+int q2_0_attn_plan_launches(const q2_0_attn_plan *plan);
+void q2_0_attn_plan_destroy(q2_0_attn_plan *plan);
+
+/*
+ * q2_0_beam_select — the selection step of a beam search: of each group's
+ * n_beams * n_vocab continuations, the n_out with the highest scores.
+ *   logits    F32, row (group, beam) at logits + (group * n_beams + beam) *
+ *             stride, n_vocab values (stride >= n_vocab, in floats). -inf and
+ *             NaN: the token may not be chosen and has no weight. +inf counts
+ *             as the largest finite value.
+ *   score     F32 [n_groups][n_beams], the beams' sums of log probabilities;
+ *             a beam of score -inf (or NaN) is not continued.
+ *   done      uint8 [n_groups][n_beams] or NULL: a finished beam (non-zero) has
+ *             one continuation, token done_token at its own score.
+ * A continuation's score is score + (x - lse) in f32, lse = m + log(sum exp(x -
+ * m)) of its row. Order: higher score first; among equals the lower beam, then
+ * the larger logit, then the lower token.
+ *   score_out, parent, token   F32, int32, int32 [n_groups][n_out]. Where fewer
+ *             than n_out continuations are possible the rest have score -inf,
+ *             parent 0 and token -1.
+ *   1 <= n_beams <= 64, 1 <= n_out <= 32, 1 <= n_vocab < 2^31 - 2^16,
+ *   n_groups * n_beams <= 65535. n_groups == 0 is a no-op.
+ * workspace: at least q2_0_beam_select_workspace_size(...) bytes of device
+ * memory, 256-byte aligned, or NULL to take it from the device's default memory
+ * pool on `stream`.
+ */
+size_t q2_0_beam_select_workspace_size(int64_t n_groups, int n_beams, int64_t n_vocab, int n_out);
+int q2_0_beam_select(const float *logits, int64_t stride, const float *score, const uint8_t *done,
+                     int done_token, int64_t n_groups, int n_beams, int64_t n_vocab, int n_out,
+                     float *score_out, int32_t *parent, int32_t *token, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * q2_0_beam_reorder — the page tables follow the selection. New beam j of a
+ * group goes on from the group's old beam p = parent[j]:
+ *   table_out[j] = table[p], len_out[j] = len[p], and the page that the next
+ *   token goes to becomes j's own: where len is a multiple of the page size,
+ *   table_out[j][len / page] = fresh[j] (if that column exists); otherwise the
+ *   first child of p keeps p's last page, and each further one gets fresh[j] with
+ *   the first len % page tokens of that page copied, in all layers. Full pages
+ *   are shared. used[j] = 1 where fresh[j] went into the table, else 0.
+ *   parent int32 [n_groups][n_beams] (index in the group); table, table_out
+ *   int32 [n_groups * n_beams][width]; len, len_out, fresh, used int32
+ *   [n_groups * n_beams]. Inputs and outputs must not overlap; the pages in
+ *   fresh are distinct and named by no row of table; a beam's last, partly
+ *   filled page is in no other row.
+ * A parent, a length (outside [0, width * page]) or a page id of a copy that is
+ * out of range leaves beam j's outputs unwritten, copies nothing and records
+ * Q2_0_DEVERR_BAD_ID with info = j. n_groups == 0 is a no-op;
+ * n_beams <= 1024, n_groups * n_beams < 2^31.
+ */
+int q2_0_beam_reorder(const q2_0_kv_cache *cache, const int32_t *parent, int64_t n_groups,
+                      int n_beams, const int32_t *table, const int32_t *len, int64_t width,
+                      const int32_t *fresh, int32_t *table_out, int32_t *len_out, int32_t *used,
+                      void *stream);
 
 /*
  * q2_0_get_error — synchronises `stream`, then reads and clears the current
