@@ -706,11 +706,11 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
     dp = None
     if done is not None:
         dp = _dev(done, "done", torch.bool if done.dtype == torch.bool else torch.uint8, G * W)
-    wp, wb = None, 0
-    if workspace is not None:
-        wb = workspace.numel()
-        wp = _dev(workspace, "workspace", torch.uint8,
-                  q2_0_beam_select_workspace_size(G, W, V, n_out))
+    wp, wb = None, q2_0_beam_select_workspace_size(G, W, V, n_out)
+    if wb > 0:
+        if workspace is None:
+            workspace = torch.empty(wb, dtype=torch.uint8, device=logits.device)
+        wp = _dev(workspace, "workspace", torch.uint8, wb)
     st = lib().q2_0_beam_select(logits.data_ptr(), stride, _dev(scores, "scores", torch.float32, G * W),
                                 dp, done_token, G, W, V, n_out,
                                 _dev(out[0], "out[0]", torch.float32, G * n_out),

@@ -93,6 +93,20 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
+                    const uint64_t (&dims)[3], const uint64_t (&strides_bytes)[2],
+                    const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn f = get_encode();
+    if (!f) return false;
+    cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+    cuuint64_t st[2] = {strides_bytes[0], strides_bytes[1]};
+    cuuint32_t b[3] = {box[0], box[1], box[2]};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return f(map, dtype, 3, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace q2
 
 using namespace q2;

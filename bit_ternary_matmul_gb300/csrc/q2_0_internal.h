@@ -31,6 +31,11 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
                     uint64_t dim1, uint64_t stride1_bytes, uint32_t box0, uint32_t box1,
                     CUtensorMapSwizzle swizzle);
 
+// As encode_tmap_2d with three dimensions.
+bool encode_tmap_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
+                    const uint64_t (&dims)[3], const uint64_t (&strides_bytes)[2],
+                    const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
+
 // ---- kernels' host launchers -------------------------------------------------
 // group: 64 (18-byte blocks) or 128 (34-byte blocks)
 cudaError_t launch_get_rows(const uint8_t *table, int64_t n_rows, int64_t K, const int32_t *ids,

@@ -47,6 +47,16 @@ __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, 
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16 (types and majors in the
+// instruction descriptor; D f32)
+__device__ __forceinline__ void tc_mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f8f6f4 (formats in the instruction descriptor)
 __device__ __forceinline__ void tc_mma_f8f6f4_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                                  uint32_t idesc, uint32_t accumulate) {
@@ -162,6 +172,18 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
     d |= uint64_t(1) << 46;
     d |= uint64_t(2) << 61;
     return d;
+}
+
+// Shared-memory matrix descriptor with all fields: byte offsets lbo and sbo,
+// layout 0 (no swizzle) or 2 (128-byte swizzle).
+//   MN-major, no swizzle: 8 x 8 core matrices (a row of 16 bytes along MN for each
+//     k); sbo from one group of 8 along MN to the next, lbo along K.
+//   MN-major, 128-byte swizzle: 64 (MN) x 8 (K) atoms of 1024 bytes; sbo from one
+//     atom to the next along K, lbo along MN.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
+                                              uint32_t layout) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t(lbo >> 4) << 16 | uint64_t(sbo >> 4) << 32 |
+           uint64_t(1) << 46 | uint64_t(layout) << 61;
 }
 
 }  // namespace q2

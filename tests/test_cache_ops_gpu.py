@@ -308,9 +308,22 @@ def test_attention(plens, lens, n_q, n_kv, dim, page, dtype):
 @pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16), (128, F16)])
 def test_attention_without_prefix_tables(dim, dtype):
     c = Attn([0], [70, 0, 300], 4, 2, dim, 16, dtype, seed=3)
-    c.plan(shared=False).execute(0)
+    plan = c.plan(shared=False)  # kept until it has run
+    plan.execute(0)
     _no_error()
     c.check()
+
+
+def test_attention_scratch_of_an_earlier_plan():
+    """Plans made one after another get the same scratch, with the earlier ones' results in it."""
+    for i in range(3):
+        for plens, lens, n_q, n_kv, dim, page, dtype in ATTN[4::3]:
+            c = Attn(plens, lens, n_q, n_kv, dim, page, dtype, seed=i)
+            plan = c.plan()
+            plan.execute(0)
+            _no_error()
+            c.check(f"{plens} {len(lens)}")
+            plan.close()
 
 
 @pytest.mark.parametrize("how", ["rising", "falling", "late_peak", "flat", "steep"])
@@ -330,7 +343,8 @@ def test_attention_score_ranges(how, dtype):
             return k * 0
         return k * 12
     c = Attn([1111], [400, 3, 129, 0], 8, 2, 128, 16, dtype, seed=11, k_of=k_of)
-    c.plan().execute(0)
+    plan = c.plan()
+    plan.execute(0)
     _no_error()
     c.check(how)
 
@@ -340,7 +354,8 @@ def test_attention_large_negative_and_zero_scale():
         c = Attn([260], [130, 1], 4, 2, 64, 16, F16, seed=5, scale=scale, k_of=k_of)
         if k_of is not None:
             c.q.copy_(c.q.abs())
-        c.plan().execute(0)
+        plan = c.plan()
+        plan.execute(0)
         _no_error()
         c.check(f"scale {scale}")
 
@@ -619,7 +634,8 @@ def test_offsets_past_32_bits():
     assert torch.equal(k[0, last], xk[:256].half().transpose(0, 1))
     assert torch.equal(v[0, last - 1, :, :44], xv[256:].half().transpose(0, 1))
     out = torch.empty_like(qr[:1])
-    q.AttnPlan(cache, qr[:1], out, table, _ints([T])).execute(0)
+    plan = q.AttnPlan(cache, qr[:1], out, table, _ints([T]))
+    plan.execute(0)
     kk, vv = xk.half().double().transpose(0, 1), xv.half().double().transpose(0, 1)
     s = qr[0].double().reshape(n_kv, 2, dim) @ kk.transpose(1, 2) * dim ** -0.5
     e = (torch.softmax(s, -1) @ vv).reshape(16, dim)
