@@ -517,6 +517,28 @@ def test_select_masks_and_odd_values():
     _check_select(wide, np.zeros((1, 4), np.float32), 4, what="wide")
 
 
+def test_select_many_rows_of_odd_shapes():
+    """Enough rows for the long pieces: sorted both ways, masked ranges, plateaus, one value far out."""
+    r = np.random.RandomState(5)
+    G, W, V = 5, 16, 151937
+    logits = (r.standard_normal((G, W, V)) * 2).astype(np.float32)
+    logits[0, :4] = np.sort(logits[0, :4], axis=-1)
+    logits[0, 4:8] = np.sort(logits[0, 4:8], axis=-1)[..., ::-1]
+    logits[1, :, : 140000] = -np.inf
+    logits[1, 3, 140000:] = -np.inf
+    logits[2, 0] = np.float32(0.5)
+    logits[2, 1:8] = np.round(logits[2, 1:8] / 4)
+    logits[2, 8, 100001] = 300.0
+    logits[2, 9, 100003] = 3e38
+    logits[2, 10] = np.finfo(np.float32).min
+    logits[2, 11, ::2] = np.finfo(np.float32).min
+    logits[3, :, ::5] = np.nan
+    scores = (-r.random((G, W)) * 3).astype(np.float32)
+    scores[2, 9:11] = -40
+    _check_select(logits, scores, 16, what="shapes")
+    _check_select(logits, scores, 32, what="shapes, 32")
+
+
 def test_select_strided_rows_workspace_and_outputs():
     r = np.random.RandomState(3)
     G, W, V = 2, 3, 1003
