@@ -115,6 +115,8 @@ def library_path() -> str:
 def lib():
     """The loaded libq2_0 (raises if it has not been built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -213,14 +215,19 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
-def _dev(t: torch.Tensor, name: str, dtype, numel: int | None = None):
+def _dev(t: torch.Tensor, name: str, dtype, numel: int = 0):
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -229,7 +236,7 @@ def _dev(t: torch.Tensor, name: str, dtype, numel: int | None = None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() < numel:
+    if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
     return t.data_ptr()
 
@@ -544,7 +551,7 @@ def _rows(t: torch.Tensor, name: str, n_tokens: int, heads: int, dim: int):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
@@ -700,9 +707,9 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
         raise ValueError("logits must have contiguous rows, evenly apart")
     n_out = W if n_out is None else n_out
     if out is None:
+        token = torch.empty((G, n_out), dtype=torch.int32, device=logits.device)
         out = (torch.empty((G, n_out), dtype=torch.float32, device=logits.device),
-               torch.empty((G, n_out), dtype=torch.int32, device=logits.device),
-               torch.empty((G, n_out), dtype=torch.int32, device=logits.device))
+               torch.empty_like(token), token)
     dp = None
     if done is not None:
         dp = _dev(done, "done", torch.bool if done.dtype == torch.bool else torch.uint8, G * W)
@@ -734,8 +741,7 @@ def q2_0_beam_reorder(cache: KvCache, parent: torch.Tensor, table: torch.Tensor,
     G, W = parent.shape
     n, width = table.shape
     if out is None:
-        out = (torch.empty_like(table), torch.empty_like(length),
-               torch.empty(n, dtype=torch.int32, device=table.device))
+        out = (torch.empty_like(table), torch.empty_like(length), torch.empty_like(length))
     st = lib().q2_0_beam_reorder(cache._ref, _dev(parent, "parent", torch.int32), G, W,
                                  _dev(table, "table", torch.int32),
                                  _dev(length, "length", torch.int32, n), width,
