@@ -2,12 +2,13 @@
 // (q2_0_attn_plan_*).
 //
 // Work. The keys of one (kv head, prefix of a group) serve all the group's query
-// heads of that kv head: rows = sequences x heads per kv head of one product. The
-// own tokens of a sequence serve its heads per kv head. Both are cut into tiles of
-// 128 keys, and the flat list of all tiles is dealt to one persistent block per SM
-// in equal, contiguous shares (a block's run of tiles of one (prefix | sequence,
-// kv head) is a segment). Every segment leaves an unnormalised output, reference
-// and sum per row; a second kernel joins the segments of each query row.
+// heads of that kv head: rows = sequences x heads per kv head of one product, in
+// blocks of up to 128. The own tokens of a sequence serve its heads per kv head. Both
+// are cut into tiles of 128 keys, and the flat list of all tiles is dealt to one
+// persistent block per SM in contiguous shares of equal cost (a block's run of tiles
+// of one (prefix | sequence, kv head, row block) is a segment). Segments leave
+// unnormalised outputs, references and sums per row; a second kernel joins those of
+// each query row.
 //
 // Products. Keys are the M of the first product and head elements the M of the
 // second, so that the tensor core's 128 rows are always full and the few query
@@ -18,12 +19,18 @@
 // product's MN-major B: a thread owns a key, and writes 16 bytes for each 8 rows.
 //
 // Softmax. p = 2^(s - ref + 7), ref a row's reference in log2 units: the maximum of
-// the segment's first tile, raised to the running maximum only when a score
-// passes it by more than 8 (then the output and sums so far are scaled down). Any
-// ref gives the same quotient; this one keeps p below 2^15 (f16's largest is 2^16)
-// and its rounding relative (normal f16) down to 2^-21 of the reference's weight,
-// and spares most tiles a reduction over their keys. Sums of p stay in registers,
-// one per (thread = key of the tile, row), and are reduced once per segment.
+// the first tile, raised to the running maximum only when a score passes it by more
+// than 8 (then the output and sums so far are scaled down). Any ref gives the same
+// quotient; this one keeps p below 2^15 (f16's largest is 2^16) and its rounding
+// relative (normal f16) down to 2^-21 of the reference's weight, and spares most tiles
+// a reduction over their keys. Sums of p stay in registers, one per (thread = key of
+// the tile, row), and are reduced once per segment.
+//
+// Two groups of four warps do the softmax. Up to 64 rows they take turns at the tiles,
+// each with scores, weights, references, sums and output of its own (two records per
+// segment): a tile's chain of steps, about 1300 clocks, is longer than its 64 KB take
+// to arrive, and so are a short segment's begin and end. With more rows each group
+// has half of them, of every tile.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -39,30 +46,36 @@ namespace q2 {
 namespace {
 
 constexpr int kTile = 128;     // keys per tile
-constexpr int kThreads = 224;  // warps: 0 K/V copies, 1 MMA, 2-5 softmax, 6 Q copies
-constexpr int kSoftThreads = 128;
+constexpr int kThreads = 384;  // warps: 0 K/V copies, 1 MMA, 2 Q copies, 4-11 softmax
+// Registers: launched with 168 per thread (64512), the first four warps leave with 88, so that
+// the softmax warps hold 64 scores and 64 sums: 128 * 88 + 256 * 208 = 64512.
+constexpr int kRegsFew = 88, kRegsMany = 208;
 constexpr int kTag = 300;      // waits' tags: 301..
 constexpr float kLift = 7.0f;  // p = 2^(s - ref + kLift)
 constexpr float kSlack = 8.0f; // how far a score may pass the reference
+// Cost of a tile, and of a segment beside its tiles, for the shares.
+constexpr int kTileCost = 4, kItemCost = 4;
 
 // Tile sizes of a variant: NCAP is the most query rows of a product.
 template <int NCAP, int D>
 struct Cfg {
+    static constexpr bool kTurns = NCAP <= 64;       // the groups take turns at the tiles
+    static constexpr int kCols = kTurns ? NCAP : 64; // most rows of a group
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kHalves = D / 64;
-    static constexpr int kQBufs = NCAP <= 64 ? 2 : 1;
-    static constexpr int kPBufs = NCAP <= 32 ? 2 : 1;
+    static constexpr int kQBufs = NCAP <= 32 ? 2 : 1;
+    static constexpr int kPBufs = kTurns ? 2 : 1;
+    static constexpr int kOBufs = kPBufs;
     static constexpr int kQBytes = NCAP * D * 2;
     static constexpr int kPBytes = NCAP * kTile * 2;
-    // what is left of 227 KB after Q, P and about 4 KB of small things
+    static constexpr int kSmall = 1024 + kPBufs * 5 * NCAP * 4 + 512;  // slack, references, barriers
     static constexpr int kStages =
-        (227 * 1024 - 5120 - kQBufs * kQBytes - kPBufs * kPBytes) / kStageBytes;
+        (227 * 1024 - kSmall - kQBufs * kQBytes - kPBufs * kPBytes) / kStageBytes;
     static constexpr int kTmemCols = NCAP == 32 ? 128 : NCAP == 64 ? 256 : 512;
     static constexpr int kOCol = 2 * NCAP;  // S buffers at 0 and NCAP
-    static constexpr int kBars = 2 * kStages + 2 * kQBufs + 4 + 2 * kPBufs + 1;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kQBufs * kQBytes +
-                                 kPBufs * kPBytes + NCAP * 4 * 6 + kBars * 8 + 128;
-    static_assert(kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
+    static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBufs * kQBytes + kPBufs * kPBytes;
+    static_assert(kStages >= 4 && kSmem + 256 <= 227 * 1024, "shared memory");
+    static_assert((2 * kStages + 2 * kQBufs + 4 + 3 * kPBufs) * 8 + 8 <= 512, "barriers");
 };
 
 struct AttnArgs {
@@ -77,9 +90,9 @@ struct AttnArgs {
     int row0;             // the layer's first row / (n_kv * page): layer * n_pages
     float scale_log2;     // scale * log2(e)
     // scratch
-    long long *start;      // [groups + seqs + 1] first tile of each owner
-    float *p_out, *s_out;  // segments' outputs: prefix [slot][NCAP][dim], own [slot][share][dim]
-    float2 *p_ml, *s_ml;   // their (reference, sum): [slot][NCAP], [slot][share]
+    long long *start;      // [groups + seqs + 1] where each owner begins in the shares' units
+    float *p_out, *s_out;  // records' outputs: prefix [rec][NCAP][dim], own [rec][share][dim]
+    float2 *p_ml, *s_ml;   // their (reference, sum): [rec][NCAP], [rec][share]; sum 0: nothing
     int grid;
     unsigned long long *err;
 };
@@ -100,13 +113,20 @@ __device__ __forceinline__ int owner_items(const AttnArgs &a, int o) {
     return o < a.n_groups ? a.n_kv * a.row_blocks : a.n_kv;
 }
 
-// T tiles in shares over G <= T blocks (none is empty, so that a tile run's segments are
-// those of consecutive blocks).
-__device__ __forceinline__ int sharers(long long T, int grid) { return T < grid ? int(T) : grid; }
-__host__ __device__ inline long long share_begin(long long c, long long T, int G) { return T * c / G; }
-// the block that tile t belongs to
-__host__ __device__ inline int share_owner(long long t, long long T, int G) {
+// T units in shares over G blocks, none smaller than a tile, so that a tile run's segments
+// are those of consecutive blocks. An item of nt tiles has kItemCost + nt * kTileCost units;
+// a tile belongs to the block that its first unit falls to.
+__device__ __forceinline__ int sharers(long long T, int grid) {
+    return int(T / kTileCost < grid ? T / kTileCost : grid);
+}
+__device__ __forceinline__ long long share_begin(long long c, long long T, int G) { return T * c / G; }
+// the block that unit t belongs to
+__device__ __forceinline__ int share_owner(long long t, long long T, int G) {
     return int(((t + 1) * G + T - 1) / T) - 1;
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ long long item_units(int nt) {
+    return nt ? kItemCost + (long long)nt * kTileCost : 0;
 }
 
 // A block's run of tiles of one item.
@@ -121,35 +141,44 @@ struct Segment {
 // Goes over a block's segments; every role does so by itself.
 struct Walk {
     int owner, len, nt;
-    long long off, left;
+    long long off, left;  // units: place in the owner, the block's rest
     __device__ __forceinline__ bool next(const AttnArgs &a, Segment &s) {
-        if (left <= 0) return false;
-        while (nt == 0) {  // terminates: left > 0 tiles lie ahead
-            ++owner;
-            off = 0;
-            len = owner_len(a, owner);
-            nt = (len + kTile - 1) / kTile;
+        while (left > 0) {
+            while (nt == 0) {  // terminates: left > 0 units lie ahead
+                ++owner;
+                off = 0;
+                len = owner_len(a, owner);
+                nt = tiles_of(len);
+            }
+            const int units = int(item_units(nt));
+            s.item = int(off / units);
+            const int u = int(off - (long long)s.item * units);  // unit of the item
+            const int n = int(left < units - u ? left : units - u);
+            off += n;
+            left -= n;
+            // tiles whose first unit lies in [u, u + n)
+            const int t0 = u <= kItemCost ? 0 : (u - kItemCost + kTileCost - 1) / kTileCost;
+            const int t1 = u + n <= kItemCost ? 0 : (u + n - kItemCost + kTileCost - 1) / kTileCost;
+            s.owner = owner;
+            s.len = len;
+            s.t0 = t0;
+            s.n = t1 - t0;
+            if (off == (long long)units * owner_items(a, owner)) nt = 0;
+            if (s.n == 0) continue;
+            if (owner < a.n_groups) {
+                s.head = s.item / a.row_blocks;
+                s.block = s.item - s.head * a.row_blocks;
+                const int seqs = a.n_seq - s.block * a.spb;
+                s.rows = (seqs < a.spb ? seqs : a.spb) * a.share;
+            } else {
+                s.head = s.item;
+                s.block = 0;
+                s.rows = a.share;
+            }
+            s.N = s.rows <= 16 ? 16 : (s.rows + 31) & ~31;
+            return true;
         }
-        s.owner = owner;
-        s.item = int(off / nt);
-        s.t0 = int(off - (long long)s.item * nt);
-        s.n = int(left < nt - s.t0 ? left : nt - s.t0);
-        s.len = len;
-        if (owner < a.n_groups) {
-            s.head = s.item / a.row_blocks;
-            s.block = s.item - s.head * a.row_blocks;
-            const int seqs = a.n_seq - s.block * a.spb;
-            s.rows = (seqs < a.spb ? seqs : a.spb) * a.share;
-        } else {
-            s.head = s.item;
-            s.block = 0;
-            s.rows = a.share;
-        }
-        s.N = s.rows <= 16 ? 16 : (s.rows + 31) & ~31;
-        off += s.n;
-        left -= s.n;
-        if (off == (long long)nt * owner_items(a, owner)) nt = 0;
-        return true;
+        return false;
     }
 };
 
@@ -168,10 +197,31 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+// Two f32 operations in one instruction.
+union Pair {
+    float2 f;
+    unsigned long long u;
+};
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    Pair p{x}, q{y}, r{z}, d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(p.u), "l"(q.u), "l"(r.u));
+    return d.f;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    Pair p{x}, q{y}, d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(p.u), "l"(q.u));
+    return d.f;
+}
+
 // Over the lanes of the warp, for W = 32 or 16 values each: lane l gets the maximum
 // (sum) of value l % W.
 template <int W, bool kMax>
-__device__ __forceinline__ float across(float (&v)[W]) {
+__device__ __forceinline__ float across(float *v) {
     const int lane = threadIdx.x & 31;
     if (W == 16) {
 #pragma unroll
@@ -192,60 +242,73 @@ __device__ __forceinline__ float across(float (&v)[W]) {
     }
     return v[0];
 }
+// The same for a row of W = 16, 32 or 64 values, into dst[0, W).
+template <int W, bool kMax>
+__device__ __forceinline__ void across_to(float (&v)[W], float *dst) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (W == 16) {
+        const float t = across<16, kMax>(v);
+        if (lane < 16) dst[lane] = t;
+    } else {
+#pragma unroll
+        for (int c = 0; c < W; c += 32) dst[c + lane] = across<32, kMax>(v + c);
+    }
+}
 
+// W = 16, 32 or 64 columns of the warp's lanes of tensor memory.
 template <int W>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[W]) {
     uint32_t r[W];
-    if constexpr (W == 32) {
-        tmem_ld32(addr, r);
-    } else {
+    if constexpr (W == 16) {
         tmem_ld16(addr, r);
-        tmem_wait_ld();
+    } else {
+#pragma unroll
+        for (int c = 0; c < W; c += 32) tmem_ld32_issue(addr + c, r + c);
     }
+    tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
 }
 template <int W>
 __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[W]) {
-    uint32_t r[W];
+    constexpr int P = W < 32 ? W : 32;
 #pragma unroll
-    for (int i = 0; i < W; ++i) r[i] = __float_as_uint(v[i]);
-    if constexpr (W == 32)
-        tmem_st32(addr, r);
-    else
-        tmem_st16(addr, r);
+    for (int c = 0; c < W; c += P) {
+        uint32_t r[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) r[i] = __float_as_uint(v[c + i]);
+        if constexpr (P == 32)
+            tmem_st32(addr + c, r);
+        else
+            tmem_st16(addr + c, r);
+    }
     tmem_wait_st();
 }
 
-// Barrier of the softmax warps.
-__device__ __forceinline__ void soft_sync() {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+// Barriers of a softmax group.
+__device__ __forceinline__ void group_sync(int w) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + 2 * w) : "memory");
 }
-__device__ __forceinline__ bool soft_any(bool v) {
+__device__ __forceinline__ bool group_any(int w, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "bar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"(uint32_t(v))
+        : "r"(uint32_t(v)), "r"(2 + 2 * w)
         : "memory");
     return r != 0;
 }
 
-// Calls f over the columns [0, N) in pieces: 16 wide if N = 16, else 32 (f is
-// instantiated for both; c is a compile-time constant after unrolling).
-template <int NCAP, typename F>
-__device__ __forceinline__ void columns(int N, F f) {
-    if (N == 16) {
-        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
-        return;
-    }
-    f(std::integral_constant<int, 32>{}, std::integral_constant<int, 0>{});
-    if constexpr (NCAP > 32)
-        if (N > 32) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
-    if constexpr (NCAP > 64) {
-        if (N > 64) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 64>{});
-        if (N > 96) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 96>{});
+// f(W) with the number of columns as a constant: 16, 32 or 64.
+template <int COLS, typename F>
+__device__ __forceinline__ void with_columns(int cols, F f) {
+    if (cols == 16) {
+        f(std::integral_constant<int, 16>{});
+    } else if (COLS == 32 || cols == 32) {
+        f(std::integral_constant<int, 32>{});
+    } else {
+        if constexpr (COLS == 64) f(std::integral_constant<int, 64>{});
     }
 }
 
@@ -258,16 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     uint8_t *ring = smem;
     uint8_t *q_s = ring + C::kStages * C::kStageBytes;
     uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
-    float *nref_s = reinterpret_cast<float *>(p_s + C::kPBufs * C::kPBytes);  // kLift - ref
-    float *alpha_s = nref_s + NCAP;
-    float *red_s = alpha_s + NCAP;  // [4][NCAP]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(red_s + 4 * NCAP);
+    float *ref_s = reinterpret_cast<float *>(p_s + C::kPBufs * C::kPBytes);  // [group's 5 NCAP]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kPBufs * 5 * NCAP);
     uint64_t *kv_full = bars, *kv_empty = kv_full + C::kStages;
     uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + C::kQBufs;
     uint64_t *s_full = q_empty + C::kQBufs, *s_empty = s_full + 2;
     uint64_t *p_full = s_empty + 2, *p_empty = p_full + C::kPBufs;
     uint64_t *o_full = p_empty + C::kPBufs;
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_full + 1);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_full + C::kOBufs);
     __shared__ long long sum_s[kThreads / 32];
     __shared__ int first_owner_s;
     __shared__ long long first_off_s;
@@ -284,13 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], 4);
+            mbar_init(&s_empty[i], C::kTurns ? 4 : 8);
         }
         for (int i = 0; i < C::kPBufs; ++i) {
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], C::kTurns ? 4 : 8);
             mbar_init(&p_empty[i], 1);
+            mbar_init(&o_full[i], 1);
         }
-        mbar_init(o_full, 1);
         fence_barrier_init();
         prefetch_tensormap(&a.k_map);
         prefetch_tensormap(&a.v_map);
@@ -314,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int o0 = min(tid * per, owners), o1 = min(o0 + per, owners);
     long long mine = 0;
     for (int o = o0; o < o1; ++o)
-        mine += (long long)((owner_len(a, o, blockIdx.x == 0) + kTile - 1) / kTile) * owner_items(a, o);
+        mine += item_units(tiles_of(owner_len(a, o, blockIdx.x == 0))) * owner_items(a, o);
     long long scan = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -335,8 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (blockIdx.x == 0 || (begin >= before && begin < before + mine)) {
         long long at = before;
         for (int o = o0; o < o1; ++o) {
-            const long long n =
-                (long long)((owner_len(a, o) + kTile - 1) / kTile) * owner_items(a, o);
+            const long long n = item_units(tiles_of(owner_len(a, o))) * owner_items(a, o);
             if (blockIdx.x == 0) a.start[o] = at;
             if (begin >= at && begin < at + n) {
                 first_owner_s = o;
@@ -357,10 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         walk.owner = first_owner_s;
         walk.off = first_off_s;
         walk.len = owner_len(a, walk.owner);
-        walk.nt = (walk.len + kTile - 1) / kTile;
+        walk.nt = tiles_of(walk.len);
     }
     Segment s;
 
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
         // ------------------------------ K and V copies ------------------------------
         const int page = 1 << a.page_shift;
@@ -415,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 }
                 mbar_wait(&kv_full[st], ph, a.err, kTag + 2);
             }
-    } else if (warp == 6) {
+    } else if (warp == 2) {
         // --------------------------------- Q copies ---------------------------------
         for (int n = 0; walk.next(a, s); ++n) {
             const int qb = n % C::kQBufs, use = n / C::kQBufs;
@@ -441,68 +502,76 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         uint32_t ph = 0;
         int n = 0;  // tiles so far
         bool ok = true;
-        // the second product of the tile before: it is issued after the next tile's first
-        bool pend = false, p_first = false, p_last = false;
-        int p_st = 0, p_steps = 0, p_n = 0, p_N = 0;
-        uint32_t p_ph = 0;
+        // Second products that wait for their weights: each is issued after the first product
+        // of the tile that comes kPBufs later.
+        struct Pending {
+            bool first, last;
+            int st, steps, n, N;
+            uint32_t ph;
+        } pend[C::kPBufs] = {};
+        int pending = 0;
         auto second = [&]() {
-            const int pb = p_n % C::kPBufs;
-            const uint32_t use = uint32_t(p_n / C::kPBufs);
-            const bool got = mbar_wait2(&kv_full[p_st], p_ph, kTag + 4, &p_full[pb], use & 1u, kTag + 5,
-                                        a.err, kWaitLimitNs);
+            const Pending p = pend[0];
+            if (C::kPBufs == 2) pend[0] = pend[C::kPBufs - 1];
+            --pending;
+            const int pb = p.n % C::kPBufs;
+            const uint32_t use = uint32_t(p.n / C::kPBufs);
+            const bool got = mbar_wait_spin(&kv_full[p.st], p.ph, a.err, kTag + 4) &&
+                             mbar_wait_spin(&p_full[pb], use & 1u, a.err, kTag + 5);
             if (!__all_sync(0xffffffffu, got)) return false;
             tc_fence_after();
             if (leader) {
                 // A = V^T: MN-major; dim 64 reads its one half twice (lanes 64.. are not used)
-                const uint32_t idesc = types | (1u << 15) | (1u << 16) | (uint32_t(p_N >> 3) << 17) |
+                const uint32_t idesc = types | (1u << 15) | (1u << 16) | (uint32_t(p.N >> 3) << 17) |
                                        (uint32_t(kTile >> 4) << 24);
-                const uint32_t va = smem_addr(ring + p_st * C::kStageBytes);
-                const uint32_t pa = smem_addr(p_s + pb * C::kPBytes);
-                for (int ks = 0; ks < p_steps; ++ks)
-                    tc_mma_f16_ss(tmem + C::kOCol,
-                                  smem_desc(va + ks * 2048, C::kHalves == 2 ? kTile * 128 : 0, 1024, 2),
-                                  smem_desc(pa + ks * 256, 128, kTile * 16, 0), idesc,
-                                  !p_first || ks > 0);
-                tc_commit(&kv_empty[p_st]);
+                const uint64_t va = smem_desc(smem_addr(ring + p.st * C::kStageBytes),
+                                              C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
+                const uint64_t pa = smem_desc(smem_addr(p_s + pb * C::kPBytes), 128, kTile * 16, 0);
+                const uint32_t o = tmem + C::kOCol + (C::kOBufs == 2 ? pb * NCAP : 0);
+                // (addresses count 16 bytes; 16 keys are 2048 bytes of V and 256 of P)
+                if (p.steps == kTile / 16) {
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, !p.first || ks > 0);
+                } else {
+                    for (int ks = 0; ks < p.steps; ++ks)
+                        tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, !p.first || ks > 0);
+                }
+                tc_commit(&kv_empty[p.st]);
                 tc_commit(&p_empty[pb]);
-                if (p_last) tc_commit(o_full);
+                if (p.last) tc_commit(&o_full[C::kOBufs == 2 ? pb : 0]);
             }
             __syncwarp();
-            pend = false;
             return true;
         };
         for (; ok && walk.next(a, s); ++seg) {
-            if (C::kQBufs == 1 && pend && !second()) {
-                ok = false;
-                break;
-            }
+            if (C::kQBufs == 1)
+                while (ok && pending) ok = second();
             const int qb = seg % C::kQBufs;
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(&q_full[qb], uint32_t(seg / C::kQBufs) & 1u, a.err, kTag + 6))) {
+            if (!ok || !__all_sync(0xffffffffu, mbar_wait_spin(&q_full[qb], uint32_t(seg / C::kQBufs) & 1u,
+                                                               a.err, kTag + 6))) {
                 ok = false;
                 break;
             }
             const uint32_t idesc =
                 types | (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
-            const uint32_t qa = smem_addr(q_s + qb * C::kQBytes);
+            const uint64_t qa = sw128_desc(smem_addr(q_s + qb * C::kQBytes));
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int sb = n & 1;
                 const uint32_t use = uint32_t(n >> 1);
-                bool got = mbar_wait(&kv_full[st], ph, a.err, kTag + 7);
-                if (use > 0) got = got && mbar_wait(&s_empty[sb], (use - 1) & 1u, a.err, kTag + 8);
+                bool got = mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 7);
+                if (use > 0) got = got && mbar_wait_spin(&s_empty[sb], (use - 1) & 1u, a.err, kTag + 8);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t ka = smem_addr(ring + st * C::kStageBytes);
+                    const uint64_t ka = sw128_desc(smem_addr(ring + st * C::kStageBytes));
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma_f16_ss(tmem + sb * NCAP,
-                                      sw128_desc(ka + (ks / 4) * (kTile * 128) + (ks % 4) * 32),
-                                      sw128_desc(qa + (ks / 4) * (NCAP * 128) + (ks % 4) * 32), idesc,
-                                      ks > 0);
+                        tc_mma_f16_ss(tmem + sb * NCAP, ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2,
+                                      qa + (ks / 4) * (NCAP * 8) + (ks % 4) * 2, idesc, ks > 0);
                     tc_commit(&kv_empty[st]);
                     tc_commit(&s_full[sb]);
                     if (i == s.n - 1) tc_commit(&q_empty[qb]);
@@ -512,197 +581,227 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     st = 0;
                     ph ^= 1u;
                 }
-                if (pend && !second()) {
+                if (pending == C::kPBufs && !second()) {
                     ok = false;
                     break;
                 }
                 const int keys = s.len - (s.t0 + i) * kTile;
-                pend = true;
-                p_first = i == 0;
-                p_last = i == s.n - 1;
-                p_steps = keys >= kTile ? kTile / 16 : (keys + 15) / 16;
-                p_st = st;
-                p_ph = ph;
-                p_n = n;
-                p_N = s.N;
+                Pending p;
+                p.first = i < C::kOBufs;
+                p.last = i >= s.n - C::kOBufs;
+                p.steps = keys >= kTile ? kTile / 16 : (keys + 15) / 16;
+                p.st = st;
+                p.ph = ph;
+                p.n = n;
+                p.N = s.N;
+                if (C::kPBufs == 2 && pending)
+                    pend[C::kPBufs - 1] = p;
+                else
+                    pend[0] = p;
+                ++pending;
                 if (++st == C::kStages) {
                     st = 0;
                     ph ^= 1u;
                 }
             }
         }
-        if (ok && pend) ok = second();
+        while (ok && pending) ok = second();
         if (!ok && leader) {
-            // the products in flight end before tensor memory is freed (bounded)
-            tc_commit(o_full);
+            // the products in flight end before tensor memory is freed: the softmax warps' wait for
+            // this one runs out after them
+            tc_commit(&o_full[0]);
         }
-    } else {
+    } else if (warp >= 4) {
         // ---------------------------------- softmax ----------------------------------
         // Thread = key `key` of the tile, or element `key` of the head in the output.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        const int w = warp >= 8;  // group
         const int quarter = warp & 3;
         const int key = quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const float c = a.scale_log2;
-        float l[NCAP];
-        int n = 0;         // tiles so far
+        const float2 scale = make_float2(a.scale_log2, a.scale_log2);
+        // of the group's rows: kLift - ref, and the four warps' [4][NCAP] to be reduced
+        float *nref_s = ref_s + (C::kTurns ? w * 5 * NCAP : 64 * w);
+        float *red_s = nref_s + NCAP;
+        float *alpha_s = red_s;  // a row's own four are read before it is written
+        const uint32_t o_col = tmem + lanes + C::kOCol + (C::kTurns ? w * NCAP : 64 * w);
+        float2 l[C::kCols / 2];
+        int n = 0, k = 0;  // tiles, and the group's, so far
+        int segs = 0;      // the group's segments so far
         int st = 1;        // the ring stage of the tile's V
         uint32_t ph = 0;
         // A warp whose wait timed out waits no more: it goes through the motions, so that
         // the barriers of the softmax warps stay matched, and its results mean nothing.
         bool dead = false;
-        auto wait = [&](uint64_t *bar, uint32_t parity, int tag) {
-            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, a.err, tag));
+        auto wait = [&](uint64_t *bar, int use, int tag) {
+            if (!dead)
+                dead = !__all_sync(0xffffffffu, mbar_wait_spin(bar, uint32_t(use) & 1u, a.err, tag));
         };
-        for (int seg = 0; walk.next(a, s); ++seg) {
-            const int N = s.N;
-#pragma unroll
-            for (int i = 0; i < NCAP; ++i) l[i] = 0.0f;
+        while (walk.next(a, s)) {
+            const int cols = C::kTurns ? s.N : max(0, min(64, s.N - 64 * w));
+            bool fresh = true;  // no tile of this segment yet
             for (int i = 0; i < s.n; ++i, ++n) {
-                const int sb = n & 1, pb = n % C::kPBufs;
+                const int v_st = st;
+                const uint32_t v_ph = ph;
+                st += 2;
+                if (st >= C::kStages) {
+                    st -= C::kStages;
+                    ph ^= 1u;
+                }
+                if (C::kTurns && (n & 1) != w) continue;
+                const int sb = n & 1, pb = C::kTurns ? w : 0;
                 const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
-                const bool in = key < keys;
-                const uint32_t sa = tmem + lanes + sb * NCAP;
-                wait(&s_full[sb], uint32_t(n >> 1), kTag + 9);
+                wait(&s_full[sb], n >> 1, kTag + 9);
                 tc_fence_after();
-                bool raise = i == 0;
-                if (!raise) {
-                    float most = -INFINITY;
-                    columns<NCAP>(N, [&](auto w, auto c0) {
-                        constexpr int W = w, C0 = c0;
-                        float v[W];
-                        tmem_load<W>(sa + C0, v);
+                if (cols == 0) {
+                    if (k > 0) wait(&p_empty[pb], k - 1, kTag + 10);
+                    if (lane == 0) mbar_arrive(&s_empty[sb]);
+                }
+                with_columns<C::kCols>(cols, [&](auto columns) {
+                    constexpr int W = columns;
+                    if (cols == 0) return;
+                    const bool in = key < keys;
+                    const uint32_t sa = tmem + lanes + sb * NCAP + (C::kTurns ? 0 : 64 * w);
+                    float v[W];
+                    auto exponents = [&]() {
 #pragma unroll
                         for (int j = 0; j < W; j += 4) {
-                            const float4 r = *reinterpret_cast<const float4 *>(nref_s + C0 + j);
-                            most = fmaxf(most, fmaxf(fmaxf(fmaf(v[j], c, r.x), fmaf(v[j + 1], c, r.y)),
-                                                     fmaxf(fmaf(v[j + 2], c, r.z), fmaf(v[j + 3], c, r.w))));
+                            const float4 r = *reinterpret_cast<const float4 *>(nref_s + j);
+                            *reinterpret_cast<float2 *>(v + j) =
+                                fma2(make_float2(v[j], v[j + 1]), scale, make_float2(r.x, r.y));
+                            *reinterpret_cast<float2 *>(v + j + 2) =
+                                fma2(make_float2(v[j + 2], v[j + 3]), scale, make_float2(r.z, r.w));
                         }
-                    });
-                    raise = soft_any(in && most > kSlack + kLift);
-                }
-                if (raise) {
-                    // the rows' maxima over the tile, and with them new references
-                    columns<NCAP>(N, [&](auto w, auto c0) {
-                        constexpr int W = w, C0 = c0;
-                        float v[W];
-                        tmem_load<W>(sa + C0, v);
+                        if (keys < kTile) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) v[j] = in ? v[j] * c : -INFINITY;
-                        const float m = across<W, true>(v);
-                        if (lane < W) red_s[quarter * NCAP + C0 + lane] = m;
-                    });
-                    soft_sync();
-                    if (key < N) {
-                        const float old = i == 0 ? -INFINITY : kLift - nref_s[key];
-                        float m = fmaxf(fmaxf(red_s[key], red_s[NCAP + key]),
-                                        fmaxf(red_s[2 * NCAP + key], red_s[3 * NCAP + key]));
-                        // no key counts (scores of -inf): any finite reference does
-                        m = fmaxf(fmaxf(m, old), -1e30f);
-                        alpha_s[key] = ex2(old - m);
-                        nref_s[key] = kLift - m;
+                            for (int j = 0; j < W; ++j) v[j] = in ? v[j] : -INFINITY;
+                        }
+                    };
+                    tmem_load<W>(sa, v);
+                    bool raise = fresh;
+                    if (!raise) {
+                        exponents();
+                        float most = v[0];
+#pragma unroll
+                        for (int j = 1; j < W - 1; j += 2) most = max3(most, v[j], v[j + 1]);
+                        raise = group_any(w, fmaxf(most, v[W - 1]) > kSlack + kLift);
+                        if (raise) tmem_load<W>(sa, v);
                     }
-                    soft_sync();
-                    if (i > 0) {
-                        wait(&p_empty[(n - 1) % C::kPBufs], uint32_t((n - 1) / C::kPBufs), kTag + 10);
-                        tc_fence_after();
-                        columns<NCAP>(N, [&](auto w, auto c0) {
-                            constexpr int W = w, C0 = c0;
-                            float v[W];
-                            tmem_load<W>(tmem + lanes + C::kOCol + C0, v);
+                    if (k > 0) wait(&p_empty[pb], k - 1, kTag + 10);
+                    if (raise) {
+                        // the rows' maxima over the tile, and with them new references
 #pragma unroll
-                            for (int j = 0; j < W; ++j) {
-                                const float f = alpha_s[C0 + j];
-                                v[j] *= f;
-                                l[C0 + j] *= f;
+                        for (int j = 0; j < W; ++j) v[j] = in ? v[j] * scale.x : -INFINITY;
+                        across_to<W, true>(v, red_s + quarter * NCAP);
+                        group_sync(w);
+                        if (key < W) {
+                            const float old = fresh ? -INFINITY : kLift - nref_s[key];
+                            float m = fmaxf(fmaxf(red_s[key], red_s[NCAP + key]),
+                                            fmaxf(red_s[2 * NCAP + key], red_s[3 * NCAP + key]));
+                            // no key counts (scores of -inf): any finite reference does
+                            m = fmaxf(fmaxf(m, old), -1e30f);
+                            alpha_s[key] = ex2(old - m);
+                            nref_s[key] = kLift - m;
+                        }
+                        group_sync(w);
+                        if (fresh) {
+#pragma unroll
+                            for (int j = 0; j < C::kCols / 2; ++j) l[j] = make_float2(0.0f, 0.0f);
+                        } else {
+                            tc_fence_after();
+                            tmem_load<W>(o_col, v);
+#pragma unroll
+                            for (int j = 0; j < W; j += 2) {
+                                const float2 f = *reinterpret_cast<const float2 *>(alpha_s + j);
+                                v[j] *= f.x;
+                                v[j + 1] *= f.y;
+                                l[j / 2].x *= f.x;
+                                l[j / 2].y *= f.y;
                             }
-                            tmem_store<W>(tmem + lanes + C::kOCol + C0, v);
-                        });
+                            tmem_store<W>(o_col, v);
+                        }
+                        tmem_load<W>(sa, v);
+                        exponents();
                     }
-                }
-                if (n >= C::kPBufs) wait(&p_empty[pb], uint32_t(n / C::kPBufs - 1), kTag + 11);
-                uint8_t *ps = p_s + pb * C::kPBytes + key * 16;
-                columns<NCAP>(N, [&](auto w, auto c0) {
-                    constexpr int W = w, C0 = c0;
-                    float v[W];
-                    tmem_load<W>(sa + C0, v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sb]);
+                    uint8_t *ps = p_s + pb * C::kPBytes + (C::kTurns ? 0 : w * 8 * (kTile * 16)) + key * 16;
 #pragma unroll
-                    for (int j = 0; j < W; j += 4) {
-                        const float4 r = *reinterpret_cast<const float4 *>(nref_s + C0 + j);
-                        v[j] = ex2(fmaf(v[j], c, r.x));
-                        v[j + 1] = ex2(fmaf(v[j + 1], c, r.y));
-                        v[j + 2] = ex2(fmaf(v[j + 2], c, r.z));
-                        v[j + 3] = ex2(fmaf(v[j + 3], c, r.w));
-                    }
+                    for (int j = 0; j < W; j += 8) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        v[j] = in ? v[j] : 0.0f;
-                        l[C0 + j] += v[j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; j += 8)
-                        *reinterpret_cast<uint4 *>(ps + ((C0 + j) / 8) * (kTile * 16)) =
+                        for (int e = 0; e < 8; e += 2) {
+                            v[j + e] = ex2(v[j + e]);
+                            v[j + e + 1] = ex2(v[j + e + 1]);
+                            l[(j + e) / 2] = add2(l[(j + e) / 2], make_float2(v[j + e], v[j + e + 1]));
+                        }
+                        *reinterpret_cast<uint4 *>(ps + (j / 8) * (kTile * 16)) =
                             make_uint4(pack<BF>(v[j], v[j + 1]), pack<BF>(v[j + 2], v[j + 3]),
                                        pack<BF>(v[j + 4], v[j + 5]), pack<BF>(v[j + 6], v[j + 7]));
+                    }
                 });
-                if (keys < kTile && (keys & 15)) {
+                if (keys < kTile && (keys & 15) && (C::kTurns || w == 0)) {
                     // places past the last key up to the product's 16: whatever V holds there,
                     // 0 times it has to be 0
-                    wait(&kv_full[st], ph, kTag + 12);
+                    wait(&kv_full[v_st], int(v_ph), kTag + 12);
                     const int n0 = 16 - (keys & 15);
-                    for (int x = key; x < n0 * C::kHalves * 8; x += kSoftThreads) {
+                    for (int x = key; x < n0 * C::kHalves * 8; x += 128) {
                         const int piece = x & 7, r = (x >> 3) / C::kHalves, h = (x >> 3) % C::kHalves;
-                        *reinterpret_cast<uint4 *>(ring + st * C::kStageBytes + h * (kTile * 128) +
+                        *reinterpret_cast<uint4 *>(ring + v_st * C::kStageBytes + h * (kTile * 128) +
                                                    (keys + r) * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&s_empty[sb]);
-                    mbar_arrive(&p_full[pb]);
-                }
-                st += 2;
-                if (st >= C::kStages) {
-                    st -= C::kStages;
-                    ph ^= 1u;
-                }
+                if (lane == 0) mbar_arrive(&p_full[pb]);
+                fresh = false;
+                ++k;
             }
             // ---- the segment's output, references and sums
             const bool pre = s.owner < a.n_groups;
             const int64_t slot =
                 (pre ? int64_t(s.owner) * a.n_kv * a.row_blocks : int64_t(s.owner - a.n_groups) * a.n_kv) +
                 s.item + blockIdx.x;
+            const int64_t rec = C::kTurns ? 2 * slot + w : slot;
             const int64_t stride = pre ? NCAP : a.share;
-            float *out = (pre ? a.p_out : a.s_out) + slot * stride * D;
-            float2 *ml = (pre ? a.p_ml : a.s_ml) + slot * stride;
-            columns<NCAP>(N, [&](auto w, auto c0) {
-                constexpr int W = w, C0 = c0;
+            const int c0 = C::kTurns ? 0 : 64 * w;  // the group's first row
+            float *out = (pre ? a.p_out : a.s_out) + (rec * stride + c0) * D;
+            float2 *ml = (pre ? a.p_ml : a.s_ml) + rec * stride + c0;
+            const int rows = min(s.rows - c0, cols);
+            if (fresh) {  // the other group had the only tile
+                if (key < rows) ml[key] = make_float2(-1e30f, 0.0f);
+                continue;
+            }
+            if (cols == 0) {
+                if (!C::kTurns) wait(&o_full[0], segs++, kTag + 13);
+                continue;
+            }
+            with_columns<C::kCols>(cols, [&](auto columns) {
+                constexpr int W = columns;
                 float v[W];
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = l[C0 + j];
-                const float t = across<W, false>(v);
-                if (lane < W) red_s[quarter * NCAP + C0 + lane] = t;
-            });
-            soft_sync();
-            if (key < s.rows)
-                ml[key] = make_float2(kLift - nref_s[key],
-                                      (red_s[key] + red_s[NCAP + key]) +
-                                          (red_s[2 * NCAP + key] + red_s[3 * NCAP + key]));
-            wait(o_full, uint32_t(seg), kTag + 13);
-            tc_fence_after();
-            columns<NCAP>(N, [&](auto w, auto c0) {
-                constexpr int W = w, C0 = c0;
-                float v[W];
-                tmem_load<W>(tmem + lanes + C::kOCol + C0, v);
-                if (key < D) {
+                for (int j = 0; j < W; j += 2) {
+                    v[j] = l[j / 2].x;
+                    v[j + 1] = l[j / 2].y;
+                }
+                across_to<W, false>(v, red_s + quarter * NCAP);
+                group_sync(w);
+                if (key < rows)
+                    ml[key] = make_float2(kLift - nref_s[key],
+                                          (red_s[key] + red_s[NCAP + key]) +
+                                              (red_s[2 * NCAP + key] + red_s[3 * NCAP + key]));
+                wait(&o_full[C::kTurns ? w : 0], segs++, kTag + 13);
+                tc_fence_after();
+                if (quarter * 32 < D) {
+                    tmem_load<W>(o_col, v);
 #pragma unroll
                     for (int j = 0; j < W; ++j)
-                        if (C0 + j < s.rows) out[(C0 + j) * D + key] = v[j];
+                        if (j < rows) out[j * D + key] = v[j];
                 }
+                tc_fence_before();
+                group_sync(w);  // nref_s and red_s are free again
             });
-            tc_fence_before();
-            soft_sync();  // nref_s and red_s are free again
         }
     }
     tc_fence_before();
@@ -713,73 +812,125 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
-// Joins the segments of each query row: one warp per row, one block per (sequence,
-// kv head).
+// Joins the records of each query row. One block per (sequence, kv head); a row's
+// records are split over `split` of the 8 warps, whose sums meet in shared memory.
 template <int D, bool BF>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a, int ncap) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int ncap,
+                                                        int recs, int split) {
+    constexpr int E = D / 32;  // elements per lane
+    __shared__ float s_m[8], s_l[8];
+    __shared__ float s_o[8][D];
     const int b = blockIdx.x, head = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = b / a.n_seq, in_group = b - group * a.n_seq;
-    const long long T = a.start[a.n_groups + a.n_groups * a.n_seq];
-    // the segments of the prefix's item and of the sequence's: slots [c0, c1] of each
-    int c0[2], c1[2];
-    int64_t slot[2];
     const int block = in_group / a.spb;
+    const int part = warp % split;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long T = a.start[a.n_groups + a.n_groups * a.n_seq];
+    // the records of the prefix's item and of the sequence's: consecutive ones
+    int np = 0, n = 0;
+    int64_t first[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         const int o = w ? a.n_groups + b : group;
         const int items = w ? a.n_kv : a.n_kv * a.row_blocks;
         const int item = w ? head : head * a.row_blocks + block;
         const long long s0 = a.start[o];
-        const long long nt = (a.start[o + 1] - s0) / items;
-        c0[w] = 0;
-        c1[w] = -1;
-        if (nt > 0) {
-            c0[w] = share_owner(s0 + item * nt, T, sharers(T, a.grid));
-            c1[w] = share_owner(s0 + item * nt + nt - 1, T, sharers(T, a.grid));
+        const long long units = (a.start[o + 1] - s0) / items;
+        first[w] = 0;
+        if (units > 0) {
+            const int G = sharers(T, a.grid);
+            const long long u = s0 + item * units;
+            const int c0 = share_owner(u + kItemCost, T, G);
+            const int c1 = share_owner(u + units - kTileCost, T, G);
+            first[w] = ((w ? int64_t(b) * a.n_kv : int64_t(group) * a.n_kv * a.row_blocks) + item + c0) *
+                       recs;
+            n += (c1 - c0 + 1) * recs;
         }
-        slot[w] = (w ? int64_t(b) * a.n_kv : int64_t(group) * a.n_kv * a.row_blocks) + item;
+        if (w == 0) np = n;
     }
-    const int np = c1[0] - c0[0] + 1, n = np + c1[1] - c0[1] + 1;
-    constexpr int E = D / 32;  // elements per lane
-    for (int r = warp; r < a.share; r += 4) {
+    for (int r0 = 0; r0 < a.share; r0 += 8 / split) {
+        const int r = r0 + warp / split;
         const int pr = (in_group - block * a.spb) * a.share + r;  // row in the prefix's item
-        auto at = [&](int i) {  // segment i's row: index into (out, ml) of its region
-            return i < np ? (slot[0] + c0[0] + i) * ncap + pr : (slot[1] + c0[1] + i - np) * a.share + r;
-        };
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, (i < np ? a.p_ml : a.s_ml)[at(i)].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float acc[E], l = 0.0f;
+        float acc[E], l = 0.0f, m = -INFINITY;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const int64_t x = at(i);
-            const float2 ml = (i < np ? a.p_ml : a.s_ml)[x];
-            const float *o = (i < np ? a.p_out : a.s_out) + x * D + lane * E;
-            const float w = ex2(ml.x - m);
-            l += w * ml.y;
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(o);
-                acc[0] += w * v.x;
-                acc[1] += w * v.y;
-                acc[E - 2] += w * v.z;
-                acc[E - 1] += w * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(o);
-                acc[0] += w * v.x;
-                acc[1] += w * v.y;
+        if (r < a.share) {
+            // 32 records at a time: lane i has the i-th's reference and sum
+            for (int i0 = part; i0 < n; i0 += 32 * split) {
+                const int i = i0 + lane * split;
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                int64_t x = 0;
+                if (i < n) {
+                    x = i < np ? (first[0] + i) * ncap + pr : (first[1] + i - np) * a.share + r;
+                    ml = __ldcg((i < np ? a.p_ml : a.s_ml) + x);
+                }
+                const float *o = (i < np ? a.p_out : a.s_out) + x * D;
+                float top = ml.x;
+#pragma unroll
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = fmaxf(top, m);
+                const float keep = ex2(m - top), mine = ml.y != 0.0f ? ex2(ml.x - top) : 0.0f;
+                m = top;
+                float sum = mine * ml.y;
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                l = l * keep + sum;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= keep;
+                const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
+                const int count = min(32, (n - i0 + split - 1) / split);
+#pragma unroll 8
+                for (int j = 0; j < count; ++j) {
+                    const float f = __shfl_sync(0xffffffffu, mine, j);
+                    const float *oj = reinterpret_cast<const float *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), j));
+                    if (live >> j & 1u) {
+                        if constexpr (E == 4) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4 *>(oj) + lane);
+                            acc[0] += f * q.x;
+                            acc[1] += f * q.y;
+                            acc[2] += f * q.z;
+                            acc[3] += f * q.w;
+                        } else {
+                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(oj) + lane);
+                            acc[0] += f * q.x;
+                            acc[1] += f * q.y;
+                        }
+                    }
+                }
             }
         }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // (NaN stays NaN)
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) +
-                                                     (int64_t(b) * a.n_q + head * a.share + r) * D +
-                                                     lane * E);
+        if (split > 1) {
+            __syncthreads();
+            if (lane == 0) {
+                s_m[warp] = m;
+                s_l[warp] = l;
+            }
 #pragma unroll
-        for (int e = 0; e < E; e += 2) dst[e / 2] = pack<BF>(acc[e] * inv, acc[e + 1] * inv);
+            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+            __syncthreads();
+            if (part == 0) {
+                for (int j = 1; j < split; ++j) m = fmaxf(m, s_m[warp + j]);
+                const float m0 = m == -INFINITY ? 0.0f : m;
+                l = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+                for (int j = 0; j < split; ++j) {
+                    const float f = ex2(s_m[warp + j] - m0);
+                    l += f * s_l[warp + j];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += f * s_o[warp + j][lane * E + e];
+                }
+            }
+        }
+        if (part == 0 && r < a.share) {
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // (NaN stays NaN)
+            uint32_t *dst = reinterpret_cast<uint32_t *>(
+                static_cast<uint16_t *>(a.out) + (int64_t(b) * a.n_q + head * a.share + r) * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) dst[e / 2] = pack<BF>(acc[e] * inv, acc[e + 1] * inv);
+        }
     }
 }
 
@@ -788,7 +939,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
 
 struct q2_0_attn_plan {
     q2::AttnArgs args;
-    int ncap, dim, n_layers, device;
+    int ncap, recs, dim, n_layers;
     bool bf;
     int64_t n_pages;
     void *scratch;
@@ -885,8 +1036,10 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
         return o;
     };
     const size_t o_start = take((size_t(a.n_groups) + seqs + 1) * 8);
-    const size_t o_p = take(p_slots * p->ncap * c.dim * 4), o_s = take(s_slots * a.share * c.dim * 4);
-    const size_t o_pml = take(p_slots * p->ncap * 8), o_sml = take(s_slots * a.share * 8);
+    const size_t recs = p->recs = p->ncap <= 64 ? 2 : 1;
+    const size_t o_p = take(recs * p_slots * p->ncap * c.dim * 4);
+    const size_t o_s = take(recs * s_slots * a.share * c.dim * 4);
+    const size_t o_pml = take(recs * p_slots * p->ncap * 8), o_sml = take(recs * s_slots * a.share * 8);
     p->scratch = nullptr;
     if (ok) ok = cudaMalloc(&p->scratch, at) == cudaSuccess;
     const Variant v = variant_of(p->ncap, p->dim, p->bf);
@@ -927,11 +1080,11 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, a);
     if (e != cudaSuccess) return cuda_status(e);
     cfg.gridDim = dim3(unsigned(a.n_groups * a.n_seq), unsigned(a.n_kv));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     auto *join = p->dim == 64 ? (p->bf ? attn_join_kernel<64, true> : attn_join_kernel<64, false>)
                               : (p->bf ? attn_join_kernel<128, true> : attn_join_kernel<128, false>);
-    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->ncap));
+    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->ncap, p->recs, a.share <= 1 ? 8 : a.share <= 2 ? 4 : a.share <= 4 ? 2 : 1));
 }
 
 int attn_plan_launches(const q2_0_attn_plan *) { return 2; }
