@@ -46,7 +46,7 @@ namespace q2 {
 namespace {
 
 constexpr int kTile = 128;     // keys per tile
-constexpr int kThreads = 384;  // warps: 0 K/V copies, 1 MMA, 2 Q copies, 4-11 softmax
+constexpr int kThreads = 384;  // warps: 0 K copies, 1 first products, 2 V copies, 3 second, 4-11 softmax
 // Registers: launched with 168 per thread (64512), the first four warps leave with 88, so that
 // the softmax warps hold 64 scores and 64 sums: 128 * 88 + 256 * 208 = 64512.
 constexpr int kRegsFew = 88, kRegsMany = 208;
@@ -64,18 +64,23 @@ struct Cfg {
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kHalves = D / 64;
     static constexpr int kQBufs = NCAP <= 32 ? 2 : 1;
-    static constexpr int kPBufs = kTurns ? 2 : 1;
-    static constexpr int kOBufs = kPBufs;
+    static constexpr int kOBufs = kTurns ? 2 : 1;
     static constexpr int kQBytes = NCAP * D * 2;
     static constexpr int kPBytes = NCAP * kTile * 2;
-    static constexpr int kSmall = 1024 + kPBufs * 5 * NCAP * 4 + 512;  // slack, references, barriers
+    static constexpr int kRefs = (kTurns ? 2 : 1) * 5 * NCAP;  // floats
+    // references, barriers, the tile list's 12 + 2 sums
+    static constexpr int kSmall = kRefs * 4 + 448;
+    // An even number: K and V then have stages of their own. (Their consumers are different warps;
+    // in a shared stage one could be a whole phase ahead of the other, which a wait by parity
+    // does not see.)
     static constexpr int kStages =
-        (227 * 1024 - kSmall - kQBufs * kQBytes - kPBufs * kPBytes) / kStageBytes;
+        (227 * 1024 - kSmall - kQBufs * kQBytes - 2 * kPBytes) / kStageBytes / 2 * 2;
     static constexpr int kTmemCols = NCAP == 32 ? 128 : NCAP == 64 ? 256 : 512;
     static constexpr int kOCol = 2 * NCAP;  // S buffers at 0 and NCAP
-    static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBufs * kQBytes + kPBufs * kPBytes;
-    static_assert(kStages >= 4 && kSmem + 256 <= 227 * 1024, "shared memory");
-    static_assert((2 * kStages + 2 * kQBufs + 4 + 3 * kPBufs) * 8 + 8 <= 512, "barriers");
+    static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes;
+    static constexpr int kBars = 2 * kStages + 2 * kQBufs + 8 + kOBufs;
+    static_assert(kStages >= 4 && kStages % 2 == 0 && kSmem <= 227 * 1024, "shared memory");
+    static_assert((kBars + 1 + kThreads / 32 + 2) * 8 <= 448, "barriers and sums");
 };
 
 struct AttnArgs {
@@ -315,23 +320,23 @@ __device__ __forceinline__ void with_columns(int cols, F f) {
 template <int NCAP, int D, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<NCAP, D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = smem;
+    extern __shared__ __align__(1024) uint8_t ring[];  // all of the block's shared memory
+    if (smem_addr(ring) & 1023u) {  // the swizzle counts on it; the 1024-byte alignment is asked for above
+        if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_TIMEOUT, kTag);
+        return;
+    }
     uint8_t *q_s = ring + C::kStages * C::kStageBytes;
     uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
-    float *ref_s = reinterpret_cast<float *>(p_s + C::kPBufs * C::kPBytes);  // [group's 5 NCAP]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kPBufs * 5 * NCAP);
+    float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 5 NCAP]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kRefs);
     uint64_t *kv_full = bars, *kv_empty = kv_full + C::kStages;
     uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + C::kQBufs;
     uint64_t *s_full = q_empty + C::kQBufs, *s_empty = s_full + 2;
-    uint64_t *p_full = s_empty + 2, *p_empty = p_full + C::kPBufs;
-    uint64_t *o_full = p_empty + C::kPBufs;
+    uint64_t *p_full = s_empty + 2, *p_empty = p_full + 2;
+    uint64_t *o_full = p_empty + 2;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_full + C::kOBufs);
-    __shared__ long long sum_s[kThreads / 32];
-    __shared__ int first_owner_s;
-    __shared__ long long first_off_s;
+    int *first_s = reinterpret_cast<int *>(tmem_ptr + 1);  // the block's first owner
+    long long *sum_s = reinterpret_cast<long long *>(o_full + C::kOBufs + 1);  // [warps], the place in the owner
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -346,12 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], C::kTurns ? 4 : 8);
-        }
-        for (int i = 0; i < C::kPBufs; ++i) {
             mbar_init(&p_full[i], C::kTurns ? 4 : 8);
             mbar_init(&p_empty[i], 1);
-            mbar_init(&o_full[i], 1);
         }
+        for (int i = 0; i < C::kOBufs; ++i) mbar_init(&o_full[i], 1);
         fence_barrier_init();
         prefetch_tensormap(&a.k_map);
         prefetch_tensormap(&a.v_map);
@@ -385,27 +388,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (lane == 31) sum_s[warp] = scan;
     __syncthreads();
     long long before = scan - mine, T = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sum_s[w];
-        T += sum_s[w];
+        const long long v = sum_s[w];
+        if (w < warp) before += v;
+        T += v;
     }
     const int G = sharers(T, gridDim.x);
     const bool has = int(blockIdx.x) < G;
     const long long begin = has ? share_begin(blockIdx.x, T, G) : T;
     const long long end = has ? share_begin(blockIdx.x + 1, T, G) : T;
-    if (blockIdx.x == 0 || (begin >= before && begin < before + mine)) {
+    if (mine && (blockIdx.x == 0 || (begin >= before && begin < before + mine))) {
         long long at = before;
         for (int o = o0; o < o1; ++o) {
-            const long long n = item_units(tiles_of(owner_len(a, o))) * owner_items(a, o);
+            const long long n =
+                o1 - o0 == 1 ? mine : item_units(tiles_of(owner_len(a, o))) * owner_items(a, o);
             if (blockIdx.x == 0) a.start[o] = at;
             if (begin >= at && begin < at + n) {
-                first_owner_s = o;
-                first_off_s = begin - at;
+                *first_s = o;
+                sum_s[kThreads / 32] = begin - at;
             }
             at += n;
         }
-        if (blockIdx.x == 0 && tid == 0) a.start[owners] = T;
+    } else if (blockIdx.x == 0) {
+        for (int o = o0; o < o1; ++o) a.start[o] = before;
     }
+    if (blockIdx.x == 0 && tid == 0) a.start[owners] = T;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -414,157 +422,124 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     Walk walk;
     walk.left = end - begin;
     if (walk.left > 0) {
-        walk.owner = first_owner_s;
-        walk.off = first_off_s;
+        walk.owner = *first_s;
+        walk.off = sum_s[kThreads / 32];
         walk.len = owner_len(a, walk.owner);
         walk.nt = tiles_of(walk.len);
     }
     Segment s;
+    // K and V alternate in the ring: from a stage to the next of its kind
+    auto next_turn = [](int &st, uint32_t &ph) {
+        if ((st += 2) >= C::kStages) {
+            st -= C::kStages;
+            ph ^= 1u;
+        }
+    };
 
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
-    if (warp == 0) {
-        // ------------------------------ K and V copies ------------------------------
+    if (warp == 0 || warp == 2) {
+        // ------------------------- K (warp 0) and V (warp 2) copies -------------------------
+        // The two take turns at the ring's stages, each from a warp of its own: with short
+        // pages the issue of a tile's copies takes longer than they do.
         const int page = 1 << a.page_shift;
         const int box = page < kTile ? page : kTile;
         const int box_bytes = box * 128;
-        int st = 0;
+        const CUtensorMap *map = warp ? &a.v_map : &a.k_map;
+        int st = warp ? 1 : 0;
         uint32_t ph = 0;
         bool ok = true;
         while (ok && walk.next(a, s)) {
             const bool pre = s.owner < a.n_groups;
             const int64_t who = pre ? s.owner : s.owner - a.n_groups;
             const int32_t *row = pre ? a.prefix_table + who * a.prefix_width : a.table + who * a.width;
+            // page ids, a lane each, in batches of 32 pages, the next batch ahead of its use
+            const int pages = (s.len + page - 1) >> a.page_shift;
+            int base = s.t0 * kTile >> a.page_shift;
+            auto ids_from = [&](int p) { return p + lane < pages ? row[p + lane] : 0; };
+            int ids = ids_from(base), more = ids_from(base + 32);
+            auto checked = [&](int id) {
+                if (id >= 0 && id < a.n_pages) return id;
+                record_error(a.err, Q2_0_DEVERR_BAD_ID, pre ? (long long)a.n_groups * a.n_seq + who : who);
+                return 0;
+            };
+            ids = checked(ids);
             for (int t = s.t0; t < s.t0 + s.n; ++t) {
                 const int left = s.len - t * kTile;
                 const int n = ((left < kTile ? left : kTile) + box - 1) / box;  // boxes with keys
                 // lane l copies box l / kHalves, columns 64 * (l % kHalves)
                 const int b = lane / C::kHalves, half = lane % C::kHalves;
-                int at = 0;
-                if (b < n) {
-                    const int key = t * kTile + b * box;
-                    int id = row[key >> a.page_shift];
-                    if (id < 0 || id >= a.n_pages) {
-                        record_error(a.err, Q2_0_DEVERR_BAD_ID,
-                                     pre ? (long long)a.n_groups * a.n_seq + who : who);
-                        id = 0;
-                    }
-                    at = (((a.row0 + id) * a.n_kv + s.head) << a.page_shift) + (key & (page - 1));
+                const int key = t * kTile + (b < n ? b : 0) * box;
+                if ((t * kTile >> a.page_shift) >= base + 32) {  // (a tile's pages lie in one batch)
+                    base += 32;
+                    ids = checked(more);
+                    more = ids_from(base + 32);
                 }
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, a.err, kTag + 1, true));
-                    if (!ok) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&kv_full[st], uint32_t(n * C::kHalves * box_bytes));
-                    __syncwarp();
-                    if (b < n)
-                        tma_load_2d(ring + st * C::kStageBytes + half * (kTile * 128) + b * box_bytes,
-                                    kv ? &a.v_map : &a.k_map, half * 64, at, &kv_full[st]);
-                    if (++st == C::kStages) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
+                const int id = __shfl_sync(0xffffffffu, ids, (key >> a.page_shift) - base);
+                const int at = (((a.row0 + id) * a.n_kv + s.head) << a.page_shift) + (key & (page - 1));
+                ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, a.err, kTag + 1, true));
                 if (!ok) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&kv_full[st], uint32_t(n * C::kHalves * box_bytes));
+                __syncwarp();
+                if (b < n)
+                    tma_load_2d(ring + st * C::kStageBytes + half * (kTile * 128) + b * box_bytes, map,
+                                half * 64, at, &kv_full[st]);
+                next_turn(st, ph);
             }
         }
         if (!ok)  // let the copies in flight land (bounded)
-            for (int k = 0; k < C::kStages; ++k) {
-                if (--st < 0) {
-                    st = C::kStages - 1;
+            for (int k = 0; k < C::kStages / 2; ++k) {
+                if ((st -= 2) < 0) {
+                    st += C::kStages;
                     ph ^= 1u;
                 }
                 mbar_wait(&kv_full[st], ph, a.err, kTag + 2);
             }
-    } else if (warp == 2) {
-        // --------------------------------- Q copies ---------------------------------
-        for (int n = 0; walk.next(a, s); ++n) {
-            const int qb = n % C::kQBufs, use = n / C::kQBufs;
-            if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[qb], uint32_t(use - 1) & 1u, a.err,
-                                                              kTag + 3, true)))
-                break;
-            if (lane == 0) {
-                const bool pre = s.owner < a.n_groups;
-                const int rows = (pre ? a.spb : 1) * a.share;  // of the box
-                const int seq = pre ? s.owner * a.n_seq + s.block * a.spb : s.owner - a.n_groups;
-                mbar_arrive_expect_tx(&q_full[qb], uint32_t(rows * D * 2));
-                for (int h = 0; h < C::kHalves; ++h)
-                    tma_load_3d(q_s + qb * C::kQBytes + h * (NCAP * 128), pre ? &a.qp_map : &a.qs_map,
-                                h * 64, s.head * a.share, seq, &q_full[qb]);
-            }
-            __syncwarp();
-        }
     } else if (warp == 1) {
-        // ------------------------------------ MMA ------------------------------------
-        const uint32_t types = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u);
+        // ----------------------- Q copies and the first products -----------------------
         const bool leader = elect_one();
         int st = 0, seg = 0;
         uint32_t ph = 0;
         int n = 0;  // tiles so far
         bool ok = true;
-        // Second products that wait for their weights: each is issued after the first product
-        // of the tile that comes kPBufs later.
-        struct Pending {
-            bool first, last;
-            int st, steps, n, N;
-            uint32_t ph;
-        } pend[C::kPBufs] = {};
-        int pending = 0;
-        auto second = [&]() {
-            const Pending p = pend[0];
-            if (C::kPBufs == 2) pend[0] = pend[C::kPBufs - 1];
-            --pending;
-            const int pb = p.n % C::kPBufs;
-            const uint32_t use = uint32_t(p.n / C::kPBufs);
-            const bool got = mbar_wait_spin(&kv_full[p.st], p.ph, a.err, kTag + 4) &&
-                             mbar_wait_spin(&p_full[pb], use & 1u, a.err, kTag + 5);
-            if (!__all_sync(0xffffffffu, got)) return false;
-            tc_fence_after();
+        // the segment's Q, into buffer seg % kQBufs
+        auto load_q = [&](const Segment &q, int i) {
+            const int qb = i % C::kQBufs, use = i / C::kQBufs;
+            if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_spin(&q_empty[qb], uint32_t(use - 1) & 1u,
+                                                                   a.err, kTag + 3)))
+                return false;
             if (leader) {
-                // A = V^T: MN-major; dim 64 reads its one half twice (lanes 64.. are not used)
-                const uint32_t idesc = types | (1u << 15) | (1u << 16) | (uint32_t(p.N >> 3) << 17) |
-                                       (uint32_t(kTile >> 4) << 24);
-                const uint64_t va = smem_desc(smem_addr(ring + p.st * C::kStageBytes),
-                                              C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
-                const uint64_t pa = smem_desc(smem_addr(p_s + pb * C::kPBytes), 128, kTile * 16, 0);
-                const uint32_t o = tmem + C::kOCol + (C::kOBufs == 2 ? pb * NCAP : 0);
-                // (addresses count 16 bytes; 16 keys are 2048 bytes of V and 256 of P)
-                if (p.steps == kTile / 16) {
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, !p.first || ks > 0);
-                } else {
-                    for (int ks = 0; ks < p.steps; ++ks)
-                        tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, !p.first || ks > 0);
-                }
-                tc_commit(&kv_empty[p.st]);
-                tc_commit(&p_empty[pb]);
-                if (p.last) tc_commit(&o_full[C::kOBufs == 2 ? pb : 0]);
+                const bool pre = q.owner < a.n_groups;
+                const int rows = (pre ? a.spb : 1) * a.share;  // of the box
+                const int seq = pre ? q.owner * a.n_seq + q.block * a.spb : q.owner - a.n_groups;
+                mbar_arrive_expect_tx(&q_full[qb], uint32_t(rows * D * 2));
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(q_s + qb * C::kQBytes + h * (NCAP * 128), pre ? &a.qp_map : &a.qs_map,
+                                h * 64, q.head * a.share, seq, &q_full[qb]);
             }
             __syncwarp();
             return true;
         };
-        for (; ok && walk.next(a, s); ++seg) {
-            if (C::kQBufs == 1)
-                while (ok && pending) ok = second();
+        Segment ahead;
+        bool more = walk.next(a, ahead);
+        if (more) ok = load_q(ahead, 0);
+        for (; ok && more; ++seg) {
+            s = ahead;
+            more = walk.next(a, ahead);
+            if (C::kQBufs == 2 && more && !(ok = load_q(ahead, seg + 1))) break;
             const int qb = seg % C::kQBufs;
-            if (!ok || !__all_sync(0xffffffffu, mbar_wait_spin(&q_full[qb], uint32_t(seg / C::kQBufs) & 1u,
-                                                               a.err, kTag + 6))) {
-                ok = false;
-                break;
-            }
-            const uint32_t idesc =
-                types | (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(&q_full[qb], uint32_t(seg / C::kQBufs) & 1u, a.err,
+                                                        kTag + 6));
+            const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) |
+                                   (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
             const uint64_t qa = sw128_desc(smem_addr(q_s + qb * C::kQBytes));
-            for (int i = 0; i < s.n; ++i, ++n) {
+            for (int i = 0; ok && i < s.n; ++i, ++n) {
                 const int sb = n & 1;
                 const uint32_t use = uint32_t(n >> 1);
-                bool got = mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 7);
-                if (use > 0) got = got && mbar_wait_spin(&s_empty[sb], (use - 1) & 1u, a.err, kTag + 8);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
+                bool got = use == 0 || mbar_wait_spin(&s_empty[sb], (use - 1) & 1u, a.err, kTag + 8);
+                got = got && mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 7);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
                 tc_fence_after();
                 if (leader) {
                     const uint64_t ka = sw128_desc(smem_addr(ring + st * C::kStageBytes));
@@ -572,45 +547,60 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     for (int ks = 0; ks < D / 16; ++ks)
                         tc_mma_f16_ss(tmem + sb * NCAP, ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2,
                                       qa + (ks / 4) * (NCAP * 8) + (ks % 4) * 2, idesc, ks > 0);
-                    tc_commit(&kv_empty[st]);
                     tc_commit(&s_full[sb]);
+                    tc_commit(&kv_empty[st]);
                     if (i == s.n - 1) tc_commit(&q_empty[qb]);
                 }
                 __syncwarp();
-                if (++st == C::kStages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-                if (pending == C::kPBufs && !second()) {
-                    ok = false;
-                    break;
-                }
+                next_turn(st, ph);
+            }
+            if (C::kQBufs == 1 && ok && more) ok = load_q(ahead, seg + 1);
+        }
+    } else if (warp == 3) {
+        // ------------------------------- the second products -------------------------------
+        const bool leader = elect_one();
+        int st = 1;
+        uint32_t ph = 0;
+        int n = 0;  // tiles so far
+        bool ok = true;
+        while (ok && walk.next(a, s)) {
+            // A = V^T: MN-major; dim 64 reads its one half twice (lanes 64.. are not used)
+            const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 15) | (1u << 16) |
+                                   (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+            for (int i = 0; i < s.n; ++i, ++n) {
+                const int pb = n & 1, ob = C::kOBufs == 2 ? pb : 0;
                 const int keys = s.len - (s.t0 + i) * kTile;
-                Pending p;
-                p.first = i < C::kOBufs;
-                p.last = i >= s.n - C::kOBufs;
-                p.steps = keys >= kTile ? kTile / 16 : (keys + 15) / 16;
-                p.st = st;
-                p.ph = ph;
-                p.n = n;
-                p.N = s.N;
-                if (C::kPBufs == 2 && pending)
-                    pend[C::kPBufs - 1] = p;
-                else
-                    pend[0] = p;
-                ++pending;
-                if (++st == C::kStages) {
-                    st = 0;
-                    ph ^= 1u;
+                const bool got = mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 4) &&
+                                 mbar_wait_spin(&p_full[pb], uint32_t(n >> 1) & 1u, a.err, kTag + 5);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t va = smem_desc(smem_addr(ring + st * C::kStageBytes),
+                                                  C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
+                    const uint64_t pa = smem_desc(smem_addr(p_s + pb * C::kPBytes), 128, kTile * 16, 0);
+                    const uint32_t o = tmem + C::kOCol + ob * NCAP;
+                    const bool add = i >= C::kOBufs;  // not the output's first
+                    // (descriptor addresses count 16 bytes: 16 keys are 2048 bytes of V and 256 of P)
+                    if (keys > kTile - 16) {
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 16; ++ks)
+                            tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, add || ks > 0);
+                    } else {
+                        for (int ks = 0; ks < (keys + 15) / 16; ++ks)
+                            tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, add || ks > 0);
+                    }
+                    tc_commit(&p_empty[pb]);
+                    tc_commit(&kv_empty[st]);
+                    if (i >= s.n - C::kOBufs) tc_commit(&o_full[ob]);
                 }
+                __syncwarp();
+                next_turn(st, ph);
             }
         }
-        while (ok && pending) ok = second();
-        if (!ok && leader) {
-            // the products in flight end before tensor memory is freed: the softmax warps' wait for
-            // this one runs out after them
-            tc_commit(&o_full[0]);
-        }
+        // the products in flight end before tensor memory is freed: the softmax warps' wait for this
+        // one runs out after them
+        if (!ok && leader) tc_commit(&o_full[0]);
     } else if (warp >= 4) {
         // ---------------------------------- softmax ----------------------------------
         // Thread = key `key` of the tile, or element `key` of the head in the output.
@@ -626,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         float *alpha_s = red_s;  // a row's own four are read before it is written
         const uint32_t o_col = tmem + lanes + C::kOCol + (C::kTurns ? w * NCAP : 64 * w);
         float2 l[C::kCols / 2];
-        int n = 0, k = 0;  // tiles, and the group's, so far
+        int n = 0;         // tiles so far
         int segs = 0;      // the group's segments so far
         int st = 1;        // the ring stage of the tile's V
         uint32_t ph = 0;
@@ -637,24 +627,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (!dead)
                 dead = !__all_sync(0xffffffffu, mbar_wait_spin(bar, uint32_t(use) & 1u, a.err, tag));
         };
+        // The output of a segment is read when the group's next weights are ready (or at the end): by
+        // then its products are done. With 64 columns there are no registers for that.
+        constexpr bool kDefer = C::kCols == 32;
+        float *o_out = nullptr;
+        int o_rows = 0, o_cols = 0;
+        auto flush = [&]() {
+            if (!o_out) return;
+            wait(&o_full[C::kTurns ? w : 0], segs++, kTag + 13);
+            tc_fence_after();
+            if (quarter * 32 < D)
+                with_columns<C::kCols>(o_cols, [&](auto columns) {
+                    constexpr int W = columns;
+                    float v[W];
+                    tmem_load<W>(o_col, v);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (j < o_rows) o_out[j * D + key] = v[j];
+                });
+            tc_fence_before();
+            o_out = nullptr;
+        };
         while (walk.next(a, s)) {
             const int cols = C::kTurns ? s.N : max(0, min(64, s.N - 64 * w));
             bool fresh = true;  // no tile of this segment yet
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int v_st = st;
                 const uint32_t v_ph = ph;
-                st += 2;
-                if (st >= C::kStages) {
-                    st -= C::kStages;
-                    ph ^= 1u;
-                }
+                next_turn(st, ph);
                 if (C::kTurns && (n & 1) != w) continue;
-                const int sb = n & 1, pb = C::kTurns ? w : 0;
+                const int sb = n & 1;  // buffer of the scores and of the weights
                 const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
                 wait(&s_full[sb], n >> 1, kTag + 9);
                 tc_fence_after();
                 if (cols == 0) {
-                    if (k > 0) wait(&p_empty[pb], k - 1, kTag + 10);
+                    if (n >= 2) wait(&p_empty[sb], (n >> 1) - 1, kTag + 10);
                     if (lane == 0) mbar_arrive(&s_empty[sb]);
                 }
                 with_columns<C::kCols>(cols, [&](auto columns) {
@@ -687,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         raise = group_any(w, fmaxf(most, v[W - 1]) > kSlack + kLift);
                         if (raise) tmem_load<W>(sa, v);
                     }
-                    if (k > 0) wait(&p_empty[pb], k - 1, kTag + 10);
                     if (raise) {
                         // the rows' maxima over the tile, and with them new references
 #pragma unroll
@@ -708,6 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 #pragma unroll
                             for (int j = 0; j < C::kCols / 2; ++j) l[j] = make_float2(0.0f, 0.0f);
                         } else {
+                            // the products into this output so far are done
+                            const int m = C::kTurns ? n - 2 : n - 1;
+                            wait(&p_empty[m & 1], m >> 1, kTag + 14);
                             tc_fence_after();
                             tmem_load<W>(o_col, v);
 #pragma unroll
@@ -726,7 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_empty[sb]);
-                    uint8_t *ps = p_s + pb * C::kPBytes + (C::kTurns ? 0 : w * 8 * (kTile * 16)) + key * 16;
+                    if (kDefer && fresh) flush();
+                    if (n >= 2) wait(&p_empty[sb], (n >> 1) - 1, kTag + 10);
+                    uint8_t *ps = p_s + sb * C::kPBytes + (C::kTurns ? 0 : w * 8 * (kTile * 16)) + key * 16;
 #pragma unroll
                     for (int j = 0; j < W; j += 8) {
 #pragma unroll
@@ -754,9 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[pb]);
+                if (lane == 0) mbar_arrive(&p_full[sb]);
                 fresh = false;
-                ++k;
             }
             // ---- the segment's output, references and sums
             const bool pre = s.owner < a.n_groups;
@@ -791,18 +801,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     ml[key] = make_float2(kLift - nref_s[key],
                                           (red_s[key] + red_s[NCAP + key]) +
                                               (red_s[2 * NCAP + key] + red_s[3 * NCAP + key]));
-                wait(&o_full[C::kTurns ? w : 0], segs++, kTag + 13);
-                tc_fence_after();
-                if (quarter * 32 < D) {
-                    tmem_load<W>(o_col, v);
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (j < rows) out[j * D + key] = v[j];
-                }
-                tc_fence_before();
                 group_sync(w);  // nref_s and red_s are free again
             });
+            o_out = out;
+            o_rows = rows;
+            o_cols = cols;
+            if (!kDefer) flush();
         }
+        flush();
     }
     tc_fence_before();
     __syncthreads();
@@ -878,26 +884,32 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 l = l * keep + sum;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] *= keep;
-                const unsigned live = __ballot_sync(0xffffffffu, ml.y != 0.0f);
+                // a record without a sum has no output either
+                const unsigned long long ptr =
+                    reinterpret_cast<unsigned long long>(ml.y != 0.0f ? o : nullptr);
                 const int count = min(32, (n - i0 + split - 1) / split);
-#pragma unroll 8
-                for (int j = 0; j < count; ++j) {
-                    const float f = __shfl_sync(0xffffffffu, mine, j);
-                    const float *oj = reinterpret_cast<const float *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), j));
-                    if (live >> j & 1u) {
-                        if constexpr (E == 4) {
-                            const float4 q = __ldcg(reinterpret_cast<const float4 *>(oj) + lane);
-                            acc[0] += f * q.x;
-                            acc[1] += f * q.y;
-                            acc[2] += f * q.z;
-                            acc[3] += f * q.w;
-                        } else {
-                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(oj) + lane);
-                            acc[0] += f * q.x;
-                            acc[1] += f * q.y;
+                for (int j0 = 0; j0 < count; j0 += 8) {  // eight loads in flight
+                    float f[8], q[8][E];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        f[j] = __shfl_sync(0xffffffffu, mine, j0 + j);
+                        const float *oj =
+                            reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, ptr, j0 + j));
+#pragma unroll
+                        for (int e = 0; e < E; ++e) q[j][e] = 0.0f;
+                        if (oj) {
+                            if constexpr (E == 4)
+                                *reinterpret_cast<float4 *>(q[j]) =
+                                    __ldcg(reinterpret_cast<const float4 *>(oj) + lane);
+                            else
+                                *reinterpret_cast<float2 *>(q[j]) =
+                                    __ldcg(reinterpret_cast<const float2 *>(oj) + lane);
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[e] += f[j] * q[j][e];
                 }
             }
         }

@@ -287,6 +287,12 @@ ATTN = [
     ([70], [5, 6, 7], 60, 20, 64, 16, F16),
     ([5003], [1, 2], 4, 2, 128, 16, BF16),
     ([3], [1] * 200, 8, 4, 64, 16, F16),
+    ([9001], [1] * 16, 16, 4, 128, 64, F16),                     # 64 rows, long
+    ([5000], [200, 0, 33] * 4, 8, 2, 64, 16, BF16),              # 48 rows
+    ([12000], [17] * 12, 8, 2, 128, 128, BF16),
+    ([9000, 4100], [i * 50 for i in range(60)], 4, 2, 64, 32, F16),
+    ([8000], [130] * 32, 8, 2, 64, 64, F16),                     # 128 rows, narrow heads
+    ([20000], [3] * 30, 4, 1, 128, 256, F16),
 ]
 
 
