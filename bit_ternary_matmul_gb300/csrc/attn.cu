@@ -95,7 +95,7 @@ struct AttnArgs {
     int row0;             // the layer's first row / (n_kv * page): layer * n_pages
     float scale_log2;     // scale * log2(e)
     // scratch
-    long long *start;      // [groups + seqs + 1] where each owner begins in the shares' units
+    int2 *p_item, *s_item; // items' records: the first one, how many (of items with keys)
     float *p_out, *s_out;  // records' outputs: prefix [rec][NCAP][dim], own [rec][share][dim]
     float2 *p_ml, *s_ml;   // their (reference, sum): [rec][NCAP], [rec][share]; sum 0: nothing
     int grid;
@@ -141,47 +141,59 @@ struct Segment {
     int t0, n;         // its tiles
     int len;           // the owner's keys
     int rows, N;       // query rows, and the product's N
+    long long at;      // the item's first unit
 };
 
 // Goes over a block's segments; every role does so by itself.
 struct Walk {
     int owner, len, nt;
-    long long off, left;  // units: place in the owner, the block's rest
+    int item, head, block, unit;  // place: unit of the item
+    long long at, end;            // unit of all, the end of the block's share
+    __device__ __forceinline__ void start(const AttnArgs &a, int o, long long off) {
+        owner = o;
+        len = owner_len(a, o);
+        nt = tiles_of(len);
+        const long long units = item_units(nt);
+        item = int(off / units);
+        unit = int(off - item * units);
+        head = o < a.n_groups ? item / a.row_blocks : item;
+        block = o < a.n_groups ? item - head * a.row_blocks : 0;
+    }
     __device__ __forceinline__ bool next(const AttnArgs &a, Segment &s) {
-        while (left > 0) {
-            while (nt == 0) {  // terminates: left > 0 units lie ahead
+        while (at < end) {
+            while (nt == 0) {  // terminates: units lie ahead
                 ++owner;
-                off = 0;
+                item = head = block = unit = 0;
                 len = owner_len(a, owner);
                 nt = tiles_of(len);
             }
             const int units = int(item_units(nt));
-            s.item = int(off / units);
-            const int u = int(off - (long long)s.item * units);  // unit of the item
-            const int n = int(left < units - u ? left : units - u);
-            off += n;
-            left -= n;
-            // tiles whose first unit lies in [u, u + n)
-            const int t0 = u <= kItemCost ? 0 : (u - kItemCost + kTileCost - 1) / kTileCost;
-            const int t1 = u + n <= kItemCost ? 0 : (u + n - kItemCost + kTileCost - 1) / kTileCost;
+            const int n = int(end - at < units - unit ? end - at : units - unit);
+            s.at = at - unit;
+            at += n;
+            const bool pre = owner < a.n_groups;
+            // tiles whose first unit lies in [unit, unit + n)
+            s.t0 = unit <= kItemCost ? 0 : (unit - kItemCost + kTileCost - 1) / kTileCost;
+            const int t1 = unit + n <= kItemCost ? 0 : (unit + n - kItemCost + kTileCost - 1) / kTileCost;
+            s.n = t1 - s.t0;
             s.owner = owner;
             s.len = len;
-            s.t0 = t0;
-            s.n = t1 - t0;
-            if (off == (long long)units * owner_items(a, owner)) nt = 0;
-            if (s.n == 0) continue;
-            if (owner < a.n_groups) {
-                s.head = s.item / a.row_blocks;
-                s.block = s.item - s.head * a.row_blocks;
-                const int seqs = a.n_seq - s.block * a.spb;
-                s.rows = (seqs < a.spb ? seqs : a.spb) * a.share;
-            } else {
-                s.head = s.item;
-                s.block = 0;
-                s.rows = a.share;
-            }
+            s.item = item;
+            s.head = head;
+            s.block = block;
+            const int seqs = a.n_seq - block * a.spb;
+            s.rows = pre ? (seqs < a.spb ? seqs : a.spb) * a.share : a.share;
             s.N = s.rows <= 16 ? 16 : (s.rows + 31) & ~31;
-            return true;
+            unit += n;
+            if (unit == units) {
+                unit = 0;
+                ++item;
+                if (!pre || ++block == a.row_blocks) {
+                    block = 0;
+                    if (++head == a.n_kv) nt = 0;
+                }
+            }
+            if (s.n) return true;
         }
         return false;
     }
@@ -398,35 +410,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const bool has = int(blockIdx.x) < G;
     const long long begin = has ? share_begin(blockIdx.x, T, G) : T;
     const long long end = has ? share_begin(blockIdx.x + 1, T, G) : T;
-    if (mine && (blockIdx.x == 0 || (begin >= before && begin < before + mine))) {
+    if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int o = o0; o < o1; ++o) {
             const long long n =
                 o1 - o0 == 1 ? mine : item_units(tiles_of(owner_len(a, o))) * owner_items(a, o);
-            if (blockIdx.x == 0) a.start[o] = at;
             if (begin >= at && begin < at + n) {
                 *first_s = o;
                 sum_s[kThreads / 32] = begin - at;
             }
             at += n;
         }
-    } else if (blockIdx.x == 0) {
-        for (int o = o0; o < o1; ++o) a.start[o] = before;
     }
-    if (blockIdx.x == 0 && tid == 0) a.start[owners] = T;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
 
     Walk walk;
-    walk.left = end - begin;
-    if (walk.left > 0) {
-        walk.owner = *first_s;
-        walk.off = sum_s[kThreads / 32];
-        walk.len = owner_len(a, walk.owner);
-        walk.nt = tiles_of(walk.len);
-    }
+    walk.at = begin;
+    walk.end = end;
+    if (begin < end) walk.start(a, *first_s, sum_s[kThreads / 32]);
     Segment s;
     // K and V alternate in the ring: from a stage to the next of its kind
     auto next_turn = [](int &st, uint32_t &ph) {
@@ -567,6 +571,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // A = V^T: MN-major; dim 64 reads its one half twice (lanes 64.. are not used)
             const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 15) | (1u << 16) |
                                    (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+            // the item's first tile is here: its records, for the join
+            if (s.t0 == 0 && leader) {
+                const bool pre = s.owner < a.n_groups;
+                const long long i =
+                    (pre ? (long long)s.owner * a.n_kv * a.row_blocks : (long long)(s.owner - a.n_groups) * a.n_kv) +
+                    s.item;
+                const int last = share_owner(s.at + item_units(tiles_of(s.len)) - kTileCost, T, G);
+                (pre ? a.p_item : a.s_item)[i] = make_int2(int((i + blockIdx.x) * C::kOBufs),
+                                                           (last - int(blockIdx.x) + 1) * C::kOBufs);
+            }
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int pb = n & 1, ob = C::kOBufs == 2 ? pb : 0;
                 const int keys = s.len - (s.t0 + i) * kTile;
@@ -818,132 +832,110 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
-// Joins the records of each query row. One block per (sequence, kv head); a row's
-// records are split over `split` of the 8 warps, whose sums meet in shared memory.
+// Joins the records of each query row: `split` warps of a block to a row, each with every
+// split-th record; their sums meet in shared memory.
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int ncap,
-                                                        int recs, int split) {
+                                                        int split) {
     constexpr int E = D / 32;  // elements per lane
     __shared__ float s_m[8], s_l[8];
     __shared__ float s_o[8][D];
-    const int b = blockIdx.x, head = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = b / a.n_seq, in_group = b - group * a.n_seq;
-    const int block = in_group / a.spb;
     const int part = warp % split;
+    const int row = int(blockIdx.x) * (8 / split) + warp / split;  // sequence * n_q + head
+    const bool live = row < a.n_groups * a.n_seq * a.n_q;
+    const int b = live ? row / a.n_q : 0, h = row - b * a.n_q;
+    const int head = h / a.share, r = h - head * a.share;
+    const int group = b / a.n_seq, in_group = b - group * a.n_seq;
+    const int block = a.prefix_width ? in_group / a.spb : 0;
+    const int pr = (in_group - block * a.spb) * a.share + r;  // row in the prefix's item
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long T = a.start[a.n_groups + a.n_groups * a.n_seq];
-    // the records of the prefix's item and of the sequence's: consecutive ones
-    int np = 0, n = 0;
-    int64_t first[2];
+    float acc[E], l = 0.0f, m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const int o = w ? a.n_groups + b : group;
-        const int items = w ? a.n_kv : a.n_kv * a.row_blocks;
-        const int item = w ? head : head * a.row_blocks + block;
-        const long long s0 = a.start[o];
-        const long long units = (a.start[o + 1] - s0) / items;
-        first[w] = 0;
-        if (units > 0) {
-            const int G = sharers(T, a.grid);
-            const long long u = s0 + item * units;
-            const int c0 = share_owner(u + kItemCost, T, G);
-            const int c1 = share_owner(u + units - kTileCost, T, G);
-            first[w] = ((w ? int64_t(b) * a.n_kv : int64_t(group) * a.n_kv * a.row_blocks) + item + c0) *
-                       recs;
-            n += (c1 - c0 + 1) * recs;
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    if (live) {
+        const int plen = owner_len(a, group), slen = owner_len(a, a.n_groups + b);
+        int2 pi = make_int2(0, 0), si = make_int2(0, 0);
+        if (plen) pi = __ldcg(a.p_item + (int64_t(group) * a.n_kv + head) * a.row_blocks + block);
+        if (slen) si = __ldcg(a.s_item + int64_t(b) * a.n_kv + head);
+        const int np = pi.y, n = np + si.y;
+        // 32 records at a time: lane i has the i-th's reference and sum
+        for (int i0 = part; i0 < n; i0 += 32 * split) {
+            const int i = i0 + lane * split;
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            const float *o = nullptr;
+            if (i < n) {
+                const int64_t x = i < np ? (int64_t(pi.x) + i) * ncap + pr
+                                         : (int64_t(si.x) + i - np) * a.share + r;
+                ml = __ldcg((i < np ? a.p_ml : a.s_ml) + x);
+                o = (i < np ? a.p_out : a.s_out) + x * D;
+            }
+            float top = ml.x;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m);
+            const float keep = ex2(m - top), mine = ml.y != 0.0f ? ex2(ml.x - top) : 0.0f;
+            m = top;
+            float sum = mine * ml.y;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = l * keep + sum;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= keep;
+            // a record without a sum has no output either
+            const unsigned long long ptr = reinterpret_cast<unsigned long long>(ml.y != 0.0f ? o : nullptr);
+            const int count = min(32, (n - i0 + split - 1) / split);
+            for (int j0 = 0; j0 < count; j0 += 8) {  // eight loads in flight
+                float f[8], q[8][E];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f[j] = __shfl_sync(0xffffffffu, mine, j0 + j);
+                    const float *oj =
+                        reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, ptr, j0 + j));
+#pragma unroll
+                    for (int e = 0; e < E; ++e) q[j][e] = 0.0f;
+                    if (oj) {
+                        if constexpr (E == 4)
+                            *reinterpret_cast<float4 *>(q[j]) =
+                                __ldcg(reinterpret_cast<const float4 *>(oj) + lane);
+                        else
+                            *reinterpret_cast<float2 *>(q[j]) =
+                                __ldcg(reinterpret_cast<const float2 *>(oj) + lane);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += f[j] * q[j][e];
+            }
         }
-        if (w == 0) np = n;
     }
-    for (int r0 = 0; r0 < a.share; r0 += 8 / split) {
-        const int r = r0 + warp / split;
-        const int pr = (in_group - block * a.spb) * a.share + r;  // row in the prefix's item
-        float acc[E], l = 0.0f, m = -INFINITY;
+    if (split > 1) {
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+        __syncthreads();
+        if (part) return;
+        for (int j = 1; j < split; ++j) m = fmaxf(m, s_m[warp + j]);
+        const float m0 = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        if (r < a.share) {
-            // 32 records at a time: lane i has the i-th's reference and sum
-            for (int i0 = part; i0 < n; i0 += 32 * split) {
-                const int i = i0 + lane * split;
-                float2 ml = make_float2(-INFINITY, 0.0f);
-                int64_t x = 0;
-                if (i < n) {
-                    x = i < np ? (first[0] + i) * ncap + pr : (first[1] + i - np) * a.share + r;
-                    ml = __ldcg((i < np ? a.p_ml : a.s_ml) + x);
-                }
-                const float *o = (i < np ? a.p_out : a.s_out) + x * D;
-                float top = ml.x;
+        for (int j = 0; j < split; ++j) {
+            const float f = ex2(s_m[warp + j] - m0);
+            l += f * s_l[warp + j];
 #pragma unroll
-                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                top = fmaxf(top, m);
-                const float keep = ex2(m - top), mine = ml.y != 0.0f ? ex2(ml.x - top) : 0.0f;
-                m = top;
-                float sum = mine * ml.y;
-#pragma unroll
-                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                l = l * keep + sum;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] *= keep;
-                // a record without a sum has no output either
-                const unsigned long long ptr =
-                    reinterpret_cast<unsigned long long>(ml.y != 0.0f ? o : nullptr);
-                const int count = min(32, (n - i0 + split - 1) / split);
-                for (int j0 = 0; j0 < count; j0 += 8) {  // eight loads in flight
-                    float f[8], q[8][E];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        f[j] = __shfl_sync(0xffffffffu, mine, j0 + j);
-                        const float *oj =
-                            reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, ptr, j0 + j));
-#pragma unroll
-                        for (int e = 0; e < E; ++e) q[j][e] = 0.0f;
-                        if (oj) {
-                            if constexpr (E == 4)
-                                *reinterpret_cast<float4 *>(q[j]) =
-                                    __ldcg(reinterpret_cast<const float4 *>(oj) + lane);
-                            else
-                                *reinterpret_cast<float2 *>(q[j]) =
-                                    __ldcg(reinterpret_cast<const float2 *>(oj) + lane);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < E; ++e) acc[e] += f[j] * q[j][e];
-                }
-            }
-        }
-        if (split > 1) {
-            __syncthreads();
-            if (lane == 0) {
-                s_m[warp] = m;
-                s_l[warp] = l;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-            __syncthreads();
-            if (part == 0) {
-                for (int j = 1; j < split; ++j) m = fmaxf(m, s_m[warp + j]);
-                const float m0 = m == -INFINITY ? 0.0f : m;
-                l = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-                for (int j = 0; j < split; ++j) {
-                    const float f = ex2(s_m[warp + j] - m0);
-                    l += f * s_l[warp + j];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += f * s_o[warp + j][lane * E + e];
-                }
-            }
-        }
-        if (part == 0 && r < a.share) {
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // (NaN stays NaN)
-            uint32_t *dst = reinterpret_cast<uint32_t *>(
-                static_cast<uint16_t *>(a.out) + (int64_t(b) * a.n_q + head * a.share + r) * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) dst[e / 2] = pack<BF>(acc[e] * inv, acc[e + 1] * inv);
+            for (int e = 0; e < E; ++e) acc[e] += f * s_o[warp + j][lane * E + e];
         }
     }
+    if (!live) return;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // (NaN stays NaN)
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + int64_t(row) * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack<BF>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 }  // namespace
@@ -951,7 +943,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 
 struct q2_0_attn_plan {
     q2::AttnArgs args;
-    int ncap, recs, dim, n_layers;
+    int ncap, dim, n_layers;
     bool bf;
     int64_t n_pages;
     void *scratch;
@@ -1047,8 +1039,9 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
         at += align256(bytes);
         return o;
     };
-    const size_t o_start = take((size_t(a.n_groups) + seqs + 1) * 8);
-    const size_t recs = p->recs = p->ncap <= 64 ? 2 : 1;
+    const size_t o_pi = take(size_t(a.n_groups) * a.n_kv * a.row_blocks * 8);
+    const size_t o_si = take(size_t(seqs) * a.n_kv * 8);
+    const size_t recs = p->ncap <= 64 ? 2 : 1;
     const size_t o_p = take(recs * p_slots * p->ncap * c.dim * 4);
     const size_t o_s = take(recs * s_slots * a.share * c.dim * 4);
     const size_t o_pml = take(recs * p_slots * p->ncap * 8), o_sml = take(recs * s_slots * a.share * 8);
@@ -1064,7 +1057,8 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
         return Q2_0_ECUDA;
     }
     char *base = static_cast<char *>(p->scratch);
-    a.start = reinterpret_cast<long long *>(base + o_start);
+    a.p_item = reinterpret_cast<int2 *>(base + o_pi);
+    a.s_item = reinterpret_cast<int2 *>(base + o_si);
     a.p_out = reinterpret_cast<float *>(base + o_p);
     a.s_out = reinterpret_cast<float *>(base + o_s);
     a.p_ml = reinterpret_cast<float2 *>(base + o_pml);
@@ -1091,12 +1085,15 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     cfg.dynamicSmemBytes = size_t(v.smem);
     cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, a);
     if (e != cudaSuccess) return cuda_status(e);
-    cfg.gridDim = dim3(unsigned(a.n_groups * a.n_seq), unsigned(a.n_kv));
+    // few rows have many records each: more warps to a row
+    const int64_t rows = int64_t(a.n_groups) * a.n_seq * a.n_q;
+    const int split = rows <= 2 * a.grid ? 8 : rows <= 4 * a.grid ? 4 : rows <= 8 * a.grid ? 2 : 1;
+    cfg.gridDim = dim3(unsigned((rows * split + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     auto *join = p->dim == 64 ? (p->bf ? attn_join_kernel<64, true> : attn_join_kernel<64, false>)
                               : (p->bf ? attn_join_kernel<128, true> : attn_join_kernel<128, false>);
-    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->ncap, p->recs, a.share <= 1 ? 8 : a.share <= 2 ? 4 : a.share <= 4 ? 2 : 1));
+    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->ncap, split));
 }
 
 int attn_plan_launches(const q2_0_attn_plan *) { return 2; }
