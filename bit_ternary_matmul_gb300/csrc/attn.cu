@@ -2,35 +2,37 @@
 // (q2_0_attn_plan_*).
 //
 // Work. The keys of one (kv head, prefix of a group) serve all the group's query
-// heads of that kv head: rows = sequences x heads per kv head of one product, in
-// blocks of up to 128. The own tokens of a sequence serve its heads per kv head. Both
-// are cut into tiles of 128 keys, and the flat list of all tiles is dealt to one
-// persistent block per SM in contiguous shares of equal cost (a block's run of tiles
-// of one (prefix | sequence, kv head, row block) is a segment). Segments leave
-// unnormalised outputs, references and sums per row; a second kernel joins those of
-// each query row.
-//
-// Products. Keys are the M of the first product and head elements the M of the
-// second, so that the tensor core's 128 rows are always full and the few query
-// rows are its N:
-//   S^T [128 keys][N] = K Q^T,   O^T [dim][N] += V^T P^T
-// K, Q and V are read from shared memory as TMA lays them down (K-major, K-major,
-// MN-major, 128-byte swizzle); P is written by the softmax warps as the second
-// product's MN-major B: a thread owns a key, and writes 16 bytes for each 8 rows.
+// heads of that kv head: rows = sequences x heads per kv head of one product. The own
+// tokens of a sequence serve its heads per kv head. Both are cut into tiles of 128
+// keys, and the flat list of all tiles is dealt to one persistent block per SM in
+// contiguous shares of equal cost (a block's run of tiles of one (prefix | sequence,
+// kv head, row block) is a segment). Segments leave unnormalised outputs, references
+// and sums per row; a last kernel joins those of each query row.
 //
 // Softmax. p = 2^(s - ref + 7), ref a row's reference in log2 units: the maximum of
 // the first tile, raised to the running maximum only when a score passes it by more
 // than 8 (then the output and sums so far are scaled down). Any ref gives the same
 // quotient; this one keeps p below 2^15 (f16's largest is 2^16) and its rounding
 // relative (normal f16) down to 2^-21 of the reference's weight, and spares most tiles
-// a reduction over their keys. Sums of p stay in registers, one per (thread = key of
-// the tile, row), and are reduced once per segment.
+// the scaling. Scores, sums and outputs are f32; p is rounded to the cache's type to be
+// the second product's operand.
 //
-// Two groups of four warps do the softmax. Up to 64 rows they take turns at the tiles,
-// each with scores, weights, references, sums and output of its own (two records per
-// segment): a tile's chain of steps, about 1300 clocks, is longer than its 64 KB take
-// to arrive, and so are a short segment's begin and end. With more rows each group
-// has half of them, of every tile.
+// Two kernels, by the rows of a product:
+//   Up to 64 (attn_kernel): keys are the M of the first product and head elements the
+//   M of the second, so that the tensor core's 128 rows are full and the few query
+//   rows are its N:  S^T [128 keys][N] = K Q^T,  O^T [dim][N] += V^T P^T.
+//   K, Q and V are read from shared memory as TMA lays them down (K-major, K-major,
+//   MN-major, 128-byte swizzle); P is written by the softmax warps as the second
+//   product's MN-major B: a thread owns a key, and writes 16 bytes for each 8 rows.
+//   Two groups of four warps take turns at the tiles, each with scores, weights,
+//   references, sums and output of its own (two records per segment): a tile's chain of
+//   steps, about 1300 clocks, is longer than half of what its 64 KB take to arrive.
+//   More (attn_rows_kernel, prefixes only): query rows are the M of both products,
+//   S [128 rows][128 keys] = Q K^T,  O [128][dim] += P V, with up to 256 rows to a tile
+//   in shared memory. A thread owns a row, so that references and sums are its own,
+//   and P stays in tensor memory, over the scores. With keys as M these products would
+//   read 128 KB and write 32 KB of shared memory per 128 rows, 1800 clocks of its
+//   bandwidth with the copies; here 64 KB per 128 rows and P not at all.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -46,9 +48,9 @@ namespace q2 {
 namespace {
 
 constexpr int kTile = 128;     // keys per tile
-constexpr int kThreads = 384;  // warps: 0 K copies, 1 first products, 2 V copies, 3 second, 4-11 softmax
+constexpr int kThreads = 384;  // 4 warps that copy and multiply, 8 of softmax
 // Registers: launched with 168 per thread (64512), the first four warps leave with 88, so that
-// the softmax warps hold 64 scores and 64 sums: 128 * 88 + 256 * 208 = 64512.
+// the softmax warps hold 128 scores: 128 * 88 + 256 * 208 = 64512.
 constexpr int kRegsFew = 88, kRegsMany = 208;
 constexpr int kTag = 300;      // waits' tags: 301..
 constexpr float kLift = 7.0f;  // p = 2^(s - ref + kLift)
@@ -56,18 +58,15 @@ constexpr float kSlack = 8.0f; // how far a score may pass the reference
 // Cost of a tile, and of a segment beside its tiles, for the shares.
 constexpr int kTileCost = 4, kItemCost = 4;
 
-// Tile sizes of a variant: NCAP is the most query rows of a product.
+// Sizes of a variant of attn_kernel: NCAP, 32 or 64, is the most query rows of a product.
 template <int NCAP, int D>
 struct Cfg {
-    static constexpr bool kTurns = NCAP <= 64;       // the groups take turns at the tiles
-    static constexpr int kCols = kTurns ? NCAP : 64; // most rows of a group
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kHalves = D / 64;
     static constexpr int kQBufs = NCAP <= 32 ? 2 : 1;
-    static constexpr int kOBufs = kTurns ? 2 : 1;
     static constexpr int kQBytes = NCAP * D * 2;
     static constexpr int kPBytes = NCAP * kTile * 2;
-    static constexpr int kRefs = (kTurns ? 2 : 1) * 5 * NCAP;  // floats
+    static constexpr int kRefs = 2 * 5 * NCAP;  // floats
     // references, barriers, the tile list's 12 + 2 sums
     static constexpr int kSmall = kRefs * 4 + 448;
     // An even number: K and V then have stages of their own. (Their consumers are different warps;
@@ -75,12 +74,28 @@ struct Cfg {
     // does not see.)
     static constexpr int kStages =
         (227 * 1024 - kSmall - kQBufs * kQBytes - 2 * kPBytes) / kStageBytes / 2 * 2;
-    static constexpr int kTmemCols = NCAP == 32 ? 128 : NCAP == 64 ? 256 : 512;
-    static constexpr int kOCol = 2 * NCAP;  // S buffers at 0 and NCAP
+    static constexpr int kTmemCols = 4 * NCAP;
+    static constexpr int kOCol = 2 * NCAP;  // S buffers at 0 and NCAP, O at 2 NCAP and 3 NCAP
     static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes;
-    static constexpr int kBars = 2 * kStages + 2 * kQBufs + 8 + kOBufs;
+    static constexpr int kBars = 2 * kStages + 2 * kQBufs + 10;
     static_assert(kStages >= 4 && kStages % 2 == 0 && kSmem <= 227 * 1024, "shared memory");
     static_assert((kBars + 1 + kThreads / 32 + 2) * 8 <= 448, "barriers and sums");
+};
+
+// Sizes of attn_rows_kernel: 256 query rows of D, two sub-blocks of 128.
+template <int D>
+struct RowsCfg {
+    static constexpr int kRows = 256;
+    static constexpr int kStageBytes = kTile * D * 2;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kSmall = 448;
+    static constexpr int kStages = (227 * 1024 - kSmall - kQBytes) / kStageBytes / 2 * 2;  // even, as above
+    static constexpr int kOCol = 256;  // S (and P) at 0 and 128, O at 256 and 384
+    static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBytes;
+    static constexpr int kBars = 2 * kStages + 2 + 6;
+    static_assert(kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
+    static_assert((kBars + 1 + kThreads / 32 + 2) * 8 <= kSmall, "barriers and sums");
 };
 
 struct AttnArgs {
@@ -91,13 +106,14 @@ struct AttnArgs {
     int64_t prefix_width, width, n_pages;
     int n_groups, n_seq, n_q, n_kv, share;
     int spb, row_blocks;  // sequences of a row block of a prefix, row blocks
-    int page_shift, dim;
+    int page_shift;
+    int own0, own1;       // the launch's owners
     int row0;             // the layer's first row / (n_kv * page): layer * n_pages
     float scale_log2;     // scale * log2(e)
     // scratch
     int2 *p_item, *s_item; // items' records: the first one, how many (of items with keys)
-    float *p_out, *s_out;  // records' outputs: prefix [rec][NCAP][dim], own [rec][share][dim]
-    float2 *p_ml, *s_ml;   // their (reference, sum): [rec][NCAP], [rec][share]; sum 0: nothing
+    float *p_out, *s_out;  // records' outputs: prefix [rec][NCAP or 128][dim], own [rec][share][dim]
+    float2 *p_ml, *s_ml;   // their (reference, sum), a row each; sum 0: nothing
     int grid;
     unsigned long long *err;
 };
@@ -329,65 +345,28 @@ __device__ __forceinline__ void with_columns(int cols, F f) {
     }
 }
 
-template <int NCAP, int D, bool BF>
-__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
-    using C = Cfg<NCAP, D>;
-    extern __shared__ __align__(1024) uint8_t ring[];  // all of the block's shared memory
-    if (smem_addr(ring) & 1023u) {  // the swizzle counts on it; the 1024-byte alignment is asked for above
-        if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_TIMEOUT, kTag);
-        return;
+// K and V alternate in a ring: from a stage to the next of its kind.
+template <int kStages>
+__device__ __forceinline__ void next_turn(int &st, uint32_t &ph) {
+    if ((st += 2) >= kStages) {
+        st -= kStages;
+        ph ^= 1u;
     }
-    uint8_t *q_s = ring + C::kStages * C::kStageBytes;
-    uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
-    float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 5 NCAP]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kRefs);
-    uint64_t *kv_full = bars, *kv_empty = kv_full + C::kStages;
-    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + C::kQBufs;
-    uint64_t *s_full = q_empty + C::kQBufs, *s_empty = s_full + 2;
-    uint64_t *p_full = s_empty + 2, *p_empty = p_full + 2;
-    uint64_t *o_full = p_empty + 2;
-    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_full + C::kOBufs);
-    int *first_s = reinterpret_cast<int *>(tmem_ptr + 1);  // the block's first owner
-    long long *sum_s = reinterpret_cast<long long *>(o_full + C::kOBufs + 1);  // [warps], the place in the owner
+}
 
+// Deals the launch's tiles: the block's share [begin, end) of all T units, over G blocks,
+// and the owner in which it begins. Each thread sums a run of owners. All threads; sum_s
+// holds kThreads / 32 + 1; the last one (the place in the owner) and *first_s are there
+// after the block's next barrier.
+struct Deal {
+    long long T, begin, end;
+    int G;
+};
+__device__ __forceinline__ Deal deal(const AttnArgs &a, long long *sum_s, int *first_s) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
-        }
-        for (int i = 0; i < C::kQBufs; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], C::kTurns ? 4 : 8);
-            mbar_init(&p_full[i], C::kTurns ? 4 : 8);
-            mbar_init(&p_empty[i], 1);
-        }
-        for (int i = 0; i < C::kOBufs; ++i) mbar_init(&o_full[i], 1);
-        fence_barrier_init();
-        prefetch_tensormap(&a.k_map);
-        prefetch_tensormap(&a.v_map);
-        prefetch_tensormap(&a.qp_map);
-        prefetch_tensormap(&a.qs_map);
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_ptr, C::kTmemCols);
-        tmem_relinquish();
-    }
-    // rows that no copy fills are zero or an earlier segment's
-    for (int i = tid; i < C::kQBufs * C::kQBytes / 16; i += kThreads)
-        reinterpret_cast<uint4 *>(q_s)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // ---- the tile list: each thread sums a run of owners, then finds the block's first tile
-    const int owners = a.n_groups + a.n_groups * a.n_seq;
+    const int owners = a.own1 - a.own0;
     const int per = (owners + kThreads - 1) / kThreads;
-    const int o0 = min(tid * per, owners), o1 = min(o0 + per, owners);
+    const int o0 = a.own0 + min(tid * per, owners), o1 = min(o0 + per, a.own1);
     long long mine = 0;
     for (int o = o0; o < o1; ++o)
         mine += item_units(tiles_of(owner_len(a, o, blockIdx.x == 0))) * owner_items(a, o);
@@ -422,83 +401,161 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             at += n;
         }
     }
+    return {T, begin, end, G};
+}
+
+// The warp's copies of K or V of the block's tiles, into every second stage of the ring from
+// `first` on. K and V have a warp each: with short pages the issue of a tile's copies takes
+// longer than they do.
+template <int D, int kStages>
+__device__ __forceinline__ void copy_tiles(const AttnArgs &a, Walk walk, const CUtensorMap *map, int first,
+                                           uint8_t *ring, uint64_t *kv_full, uint64_t *kv_empty) {
+    constexpr int kHalves = D / 64, kStageBytes = kTile * D * 2;
+    const int lane = threadIdx.x & 31;
+    Segment s;
+    const int page = 1 << a.page_shift;
+    const int box = page < kTile ? page : kTile;
+    const int box_bytes = box * 128;
+    int st = first;
+    uint32_t ph = 0;
+    bool ok = true;
+    while (ok && walk.next(a, s)) {
+        const bool pre = s.owner < a.n_groups;
+        const int64_t who = pre ? s.owner : s.owner - a.n_groups;
+        const int32_t *row = pre ? a.prefix_table + who * a.prefix_width : a.table + who * a.width;
+        // page ids, a lane each, in batches of 32 pages, the next batch ahead of its use
+        const int pages = (s.len + page - 1) >> a.page_shift;
+        int base = s.t0 * kTile >> a.page_shift;
+        auto ids_from = [&](int p) { return p + lane < pages ? row[p + lane] : 0; };
+        int ids = ids_from(base), more = ids_from(base + 32);
+        auto checked = [&](int id) {
+            if (id >= 0 && id < a.n_pages) return id;
+            record_error(a.err, Q2_0_DEVERR_BAD_ID, pre ? (long long)a.n_groups * a.n_seq + who : who);
+            return 0;
+        };
+        ids = checked(ids);
+        for (int t = s.t0; t < s.t0 + s.n; ++t) {
+            const int left = s.len - t * kTile;
+            const int n = ((left < kTile ? left : kTile) + box - 1) / box;  // boxes with keys
+            // lane l copies box l / kHalves, columns 64 * (l % kHalves)
+            const int b = lane / kHalves, half = lane % kHalves;
+            const int key = t * kTile + (b < n ? b : 0) * box;
+            if ((t * kTile >> a.page_shift) >= base + 32) {  // (a tile's pages lie in one batch)
+                base += 32;
+                ids = checked(more);
+                more = ids_from(base + 32);
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, (key >> a.page_shift) - base);
+            const int at = (((a.row0 + id) * a.n_kv + s.head) << a.page_shift) + (key & (page - 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, a.err, kTag + 1, true));
+            if (!ok) break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&kv_full[st], uint32_t(n * kHalves * box_bytes));
+            __syncwarp();
+            if (b < n)
+                tma_load_2d(ring + st * kStageBytes + half * (kTile * 128) + b * box_bytes, map,
+                            half * 64, at, &kv_full[st]);
+            next_turn<kStages>(st, ph);
+        }
+    }
+    if (!ok)  // let the copies in flight land (bounded)
+        for (int k = 0; k < kStages / 2; ++k) {
+            if ((st -= 2) < 0) {
+                st += kStages;
+                ph ^= 1u;
+            }
+            mbar_wait(&kv_full[st], ph, a.err, kTag + 2);
+        }
+}
+
+// The item whose first tile is this segment's: where its records are, for the join.
+__device__ __forceinline__ void note_item(const AttnArgs &a, const Segment &s, const Deal &d) {
+    const bool pre = s.owner < a.n_groups;
+    const long long i =
+        (pre ? (long long)s.owner * a.n_kv * a.row_blocks : (long long)(s.owner - a.n_groups) * a.n_kv) +
+        s.item;
+    const int last = share_owner(s.at + item_units(tiles_of(s.len)) - kTileCost, d.T, d.G);
+    (pre ? a.p_item : a.s_item)[i] =
+        make_int2(int((i + blockIdx.x) * 2), (last - int(blockIdx.x) + 1) * 2);
+}
+// The segment's first record (it has two).
+__device__ __forceinline__ int64_t record_of(const AttnArgs &a, const Segment &s) {
+    const int64_t i = s.owner < a.n_groups ? int64_t(s.owner) * a.n_kv * a.row_blocks
+                                           : int64_t(s.owner - a.n_groups) * a.n_kv;
+    return 2 * (i + s.item + blockIdx.x);
+}
+
+template <int NCAP, int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+    using C = Cfg<NCAP, D>;
+    extern __shared__ __align__(1024) uint8_t ring[];  // all of the block's shared memory
+    if (smem_addr(ring) & 1023u) {  // the swizzle counts on it; the 1024-byte alignment is asked for above
+        if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_TIMEOUT, kTag);
+        return;
+    }
+    uint8_t *q_s = ring + C::kStages * C::kStageBytes;
+    uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
+    float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 5 NCAP]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kRefs);
+    uint64_t *kv_full = bars, *kv_empty = kv_full + C::kStages;
+    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + C::kQBufs;
+    uint64_t *s_full = q_empty + C::kQBufs, *s_empty = s_full + 2;
+    uint64_t *p_full = s_empty + 2, *p_empty = p_full + 2;
+    uint64_t *o_full = p_empty + 2;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_full + 2);
+    int *first_s = reinterpret_cast<int *>(tmem_ptr + 1);  // the block's first owner
+    long long *sum_s = reinterpret_cast<long long *>(o_full + 2 + 1);  // [warps], the place in the owner
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < C::kQBufs; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 4);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&p_empty[i], 1);
+            mbar_init(&o_full[i], 1);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&a.k_map);
+        prefetch_tensormap(&a.v_map);
+        prefetch_tensormap(&a.qp_map);
+        prefetch_tensormap(&a.qs_map);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_ptr, C::kTmemCols);
+        tmem_relinquish();
+    }
+    // rows that no copy fills are zero or an earlier segment's
+    for (int i = tid; i < C::kQBufs * C::kQBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Behind attn_rows_kernel (own0 > 0) this launch begins when all blocks of that one have seen
+    // the call's inputs complete, runs beside its last blocks, and waits for it before it ends.
+    if (a.own0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Deal dealt = deal(a, sum_s, first_s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
 
     Walk walk;
-    walk.at = begin;
-    walk.end = end;
-    if (begin < end) walk.start(a, *first_s, sum_s[kThreads / 32]);
+    walk.at = dealt.begin;
+    walk.end = dealt.end;
+    if (walk.at < walk.end) walk.start(a, *first_s, sum_s[kThreads / 32]);
     Segment s;
-    // K and V alternate in the ring: from a stage to the next of its kind
-    auto next_turn = [](int &st, uint32_t &ph) {
-        if ((st += 2) >= C::kStages) {
-            st -= C::kStages;
-            ph ^= 1u;
-        }
-    };
-
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0 || warp == 2) {
         // ------------------------- K (warp 0) and V (warp 2) copies -------------------------
-        // The two take turns at the ring's stages, each from a warp of its own: with short
-        // pages the issue of a tile's copies takes longer than they do.
-        const int page = 1 << a.page_shift;
-        const int box = page < kTile ? page : kTile;
-        const int box_bytes = box * 128;
-        const CUtensorMap *map = warp ? &a.v_map : &a.k_map;
-        int st = warp ? 1 : 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && walk.next(a, s)) {
-            const bool pre = s.owner < a.n_groups;
-            const int64_t who = pre ? s.owner : s.owner - a.n_groups;
-            const int32_t *row = pre ? a.prefix_table + who * a.prefix_width : a.table + who * a.width;
-            // page ids, a lane each, in batches of 32 pages, the next batch ahead of its use
-            const int pages = (s.len + page - 1) >> a.page_shift;
-            int base = s.t0 * kTile >> a.page_shift;
-            auto ids_from = [&](int p) { return p + lane < pages ? row[p + lane] : 0; };
-            int ids = ids_from(base), more = ids_from(base + 32);
-            auto checked = [&](int id) {
-                if (id >= 0 && id < a.n_pages) return id;
-                record_error(a.err, Q2_0_DEVERR_BAD_ID, pre ? (long long)a.n_groups * a.n_seq + who : who);
-                return 0;
-            };
-            ids = checked(ids);
-            for (int t = s.t0; t < s.t0 + s.n; ++t) {
-                const int left = s.len - t * kTile;
-                const int n = ((left < kTile ? left : kTile) + box - 1) / box;  // boxes with keys
-                // lane l copies box l / kHalves, columns 64 * (l % kHalves)
-                const int b = lane / C::kHalves, half = lane % C::kHalves;
-                const int key = t * kTile + (b < n ? b : 0) * box;
-                if ((t * kTile >> a.page_shift) >= base + 32) {  // (a tile's pages lie in one batch)
-                    base += 32;
-                    ids = checked(more);
-                    more = ids_from(base + 32);
-                }
-                const int id = __shfl_sync(0xffffffffu, ids, (key >> a.page_shift) - base);
-                const int at = (((a.row0 + id) * a.n_kv + s.head) << a.page_shift) + (key & (page - 1));
-                ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, a.err, kTag + 1, true));
-                if (!ok) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&kv_full[st], uint32_t(n * C::kHalves * box_bytes));
-                __syncwarp();
-                if (b < n)
-                    tma_load_2d(ring + st * C::kStageBytes + half * (kTile * 128) + b * box_bytes, map,
-                                half * 64, at, &kv_full[st]);
-                next_turn(st, ph);
-            }
-        }
-        if (!ok)  // let the copies in flight land (bounded)
-            for (int k = 0; k < C::kStages / 2; ++k) {
-                if ((st -= 2) < 0) {
-                    st += C::kStages;
-                    ph ^= 1u;
-                }
-                mbar_wait(&kv_full[st], ph, a.err, kTag + 2);
-            }
+        copy_tiles<D, C::kStages>(a, walk, warp ? &a.v_map : &a.k_map, warp ? 1 : 0, ring, kv_full, kv_empty);
     } else if (warp == 1) {
         // ----------------------- Q copies and the first products -----------------------
         const bool leader = elect_one();
@@ -556,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (i == s.n - 1) tc_commit(&q_empty[qb]);
                 }
                 __syncwarp();
-                next_turn(st, ph);
+                next_turn<C::kStages>(st, ph);
             }
             if (C::kQBufs == 1 && ok && more) ok = load_q(ahead, seg + 1);
         }
@@ -571,18 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // A = V^T: MN-major; dim 64 reads its one half twice (lanes 64.. are not used)
             const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 15) | (1u << 16) |
                                    (uint32_t(s.N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
-            // the item's first tile is here: its records, for the join
-            if (s.t0 == 0 && leader) {
-                const bool pre = s.owner < a.n_groups;
-                const long long i =
-                    (pre ? (long long)s.owner * a.n_kv * a.row_blocks : (long long)(s.owner - a.n_groups) * a.n_kv) +
-                    s.item;
-                const int last = share_owner(s.at + item_units(tiles_of(s.len)) - kTileCost, T, G);
-                (pre ? a.p_item : a.s_item)[i] = make_int2(int((i + blockIdx.x) * C::kOBufs),
-                                                           (last - int(blockIdx.x) + 1) * C::kOBufs);
-            }
+            if (s.t0 == 0 && leader) note_item(a, s, dealt);
             for (int i = 0; i < s.n; ++i, ++n) {
-                const int pb = n & 1, ob = C::kOBufs == 2 ? pb : 0;
+                const int pb = n & 1;
                 const int keys = s.len - (s.t0 + i) * kTile;
                 const bool got = mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 4) &&
                                  mbar_wait_spin(&p_full[pb], uint32_t(n >> 1) & 1u, a.err, kTag + 5);
@@ -593,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const uint64_t va = smem_desc(smem_addr(ring + st * C::kStageBytes),
                                                   C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
                     const uint64_t pa = smem_desc(smem_addr(p_s + pb * C::kPBytes), 128, kTile * 16, 0);
-                    const uint32_t o = tmem + C::kOCol + ob * NCAP;
-                    const bool add = i >= C::kOBufs;  // not the output's first
+                    const uint32_t o = tmem + C::kOCol + pb * NCAP;
+                    const bool add = i >= 2;  // not its output's first
                     // (descriptor addresses count 16 bytes: 16 keys are 2048 bytes of V and 256 of P)
                     if (keys > kTile - 16) {
 #pragma unroll
@@ -606,10 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     }
                     tc_commit(&p_empty[pb]);
                     tc_commit(&kv_empty[st]);
-                    if (i >= s.n - C::kOBufs) tc_commit(&o_full[ob]);
+                    if (i >= s.n - 2) tc_commit(&o_full[pb]);
                 }
                 __syncwarp();
-                next_turn(st, ph);
+                next_turn<C::kStages>(st, ph);
             }
         }
         // the products in flight end before tensor memory is freed: the softmax warps' wait for this
@@ -625,11 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const float2 scale = make_float2(a.scale_log2, a.scale_log2);
         // of the group's rows: kLift - ref, and the four warps' [4][NCAP] to be reduced
-        float *nref_s = ref_s + (C::kTurns ? w * 5 * NCAP : 64 * w);
+        float *nref_s = ref_s + w * 5 * NCAP;
         float *red_s = nref_s + NCAP;
         float *alpha_s = red_s;  // a row's own four are read before it is written
-        const uint32_t o_col = tmem + lanes + C::kOCol + (C::kTurns ? w * NCAP : 64 * w);
-        float2 l[C::kCols / 2];
+        const uint32_t o_col = tmem + lanes + C::kOCol + w * NCAP;
+        float2 l[NCAP / 2];
         int n = 0;         // tiles so far
         int segs = 0;      // the group's segments so far
         int st = 1;        // the ring stage of the tile's V
@@ -643,15 +691,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         };
         // The output of a segment is read when the group's next weights are ready (or at the end): by
         // then its products are done. With 64 columns there are no registers for that.
-        constexpr bool kDefer = C::kCols == 32;
+        constexpr bool kDefer = NCAP == 32;
         float *o_out = nullptr;
         int o_rows = 0, o_cols = 0;
         auto flush = [&]() {
             if (!o_out) return;
-            wait(&o_full[C::kTurns ? w : 0], segs++, kTag + 13);
+            wait(&o_full[w], segs++, kTag + 13);
             tc_fence_after();
             if (quarter * 32 < D)
-                with_columns<C::kCols>(o_cols, [&](auto columns) {
+                with_columns<NCAP>(o_cols, [&](auto columns) {
                     constexpr int W = columns;
                     float v[W];
                     tmem_load<W>(o_col, v);
@@ -663,26 +711,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             o_out = nullptr;
         };
         while (walk.next(a, s)) {
-            const int cols = C::kTurns ? s.N : max(0, min(64, s.N - 64 * w));
             bool fresh = true;  // no tile of this segment yet
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int v_st = st;
                 const uint32_t v_ph = ph;
-                next_turn(st, ph);
-                if (C::kTurns && (n & 1) != w) continue;
-                const int sb = n & 1;  // buffer of the scores and of the weights
+                next_turn<C::kStages>(st, ph);
+                if ((n & 1) != w) continue;
+                // (the group's buffers of scores, weights and outputs are number w)
                 const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
-                wait(&s_full[sb], n >> 1, kTag + 9);
+                wait(&s_full[w], n >> 1, kTag + 9);
                 tc_fence_after();
-                if (cols == 0) {
-                    if (n >= 2) wait(&p_empty[sb], (n >> 1) - 1, kTag + 10);
-                    if (lane == 0) mbar_arrive(&s_empty[sb]);
-                }
-                with_columns<C::kCols>(cols, [&](auto columns) {
+                with_columns<NCAP>(s.N, [&](auto columns) {
                     constexpr int W = columns;
-                    if (cols == 0) return;
                     const bool in = key < keys;
-                    const uint32_t sa = tmem + lanes + sb * NCAP + (C::kTurns ? 0 : 64 * w);
+                    const uint32_t sa = tmem + lanes + w * NCAP;
                     float v[W];
                     auto exponents = [&]() {
 #pragma unroll
@@ -726,11 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         group_sync(w);
                         if (fresh) {
 #pragma unroll
-                            for (int j = 0; j < C::kCols / 2; ++j) l[j] = make_float2(0.0f, 0.0f);
+                            for (int j = 0; j < NCAP / 2; ++j) l[j] = make_float2(0.0f, 0.0f);
                         } else {
                             // the products into this output so far are done
-                            const int m = C::kTurns ? n - 2 : n - 1;
-                            wait(&p_empty[m & 1], m >> 1, kTag + 14);
+                            wait(&p_empty[w], (n >> 1) - 1, kTag + 14);
                             tc_fence_after();
                             tmem_load<W>(o_col, v);
 #pragma unroll
@@ -748,10 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[sb]);
+                    if (lane == 0) mbar_arrive(&s_empty[w]);
                     if (kDefer && fresh) flush();
-                    if (n >= 2) wait(&p_empty[sb], (n >> 1) - 1, kTag + 10);
-                    uint8_t *ps = p_s + sb * C::kPBytes + (C::kTurns ? 0 : w * 8 * (kTile * 16)) + key * 16;
+                    if (n >= 2) wait(&p_empty[w], (n >> 1) - 1, kTag + 10);
+                    uint8_t *ps = p_s + w * C::kPBytes + key * 16;
 #pragma unroll
                     for (int j = 0; j < W; j += 8) {
 #pragma unroll
@@ -765,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                        pack<BF>(v[j + 4], v[j + 5]), pack<BF>(v[j + 6], v[j + 7]));
                     }
                 });
-                if (keys < kTile && (keys & 15) && (C::kTurns || w == 0)) {
+                if (keys < kTile && (keys & 15)) {
                     // places past the last key up to the product's 16: whatever V holds there,
                     // 0 times it has to be 0
                     wait(&kv_full[v_st], int(v_ph), kTag + 12);
@@ -779,29 +820,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[sb]);
+                if (lane == 0) mbar_arrive(&p_full[w]);
                 fresh = false;
             }
             // ---- the segment's output, references and sums
             const bool pre = s.owner < a.n_groups;
-            const int64_t slot =
-                (pre ? int64_t(s.owner) * a.n_kv * a.row_blocks : int64_t(s.owner - a.n_groups) * a.n_kv) +
-                s.item + blockIdx.x;
-            const int64_t rec = C::kTurns ? 2 * slot + w : slot;
-            const int64_t stride = pre ? NCAP : a.share;
-            const int c0 = C::kTurns ? 0 : 64 * w;  // the group's first row
-            float *out = (pre ? a.p_out : a.s_out) + (rec * stride + c0) * D;
-            float2 *ml = (pre ? a.p_ml : a.s_ml) + rec * stride + c0;
-            const int rows = min(s.rows - c0, cols);
+            const int64_t at = (record_of(a, s) + w) * (pre ? NCAP : a.share);
+            float *out = (pre ? a.p_out : a.s_out) + at * D;
+            float2 *ml = (pre ? a.p_ml : a.s_ml) + at;
+            const int rows = s.rows;
             if (fresh) {  // the other group had the only tile
                 if (key < rows) ml[key] = make_float2(-1e30f, 0.0f);
                 continue;
             }
-            if (cols == 0) {
-                if (!C::kTurns) wait(&o_full[0], segs++, kTag + 13);
-                continue;
-            }
-            with_columns<C::kCols>(cols, [&](auto columns) {
+            with_columns<NCAP>(s.N, [&](auto columns) {
                 constexpr int W = columns;
                 float v[W];
 #pragma unroll
@@ -819,11 +851,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             });
             o_out = out;
             o_rows = rows;
-            o_cols = cols;
+            o_cols = s.N;
             if (!kDefer) flush();
         }
         flush();
     }
+    if (a.own0) asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -832,11 +865,310 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
 }
 
+// Prefixes with more than 64 query rows: see the top of the file. Of a row block of up to 256
+// rows, softmax group w has rows 128 w .. 127 + 128 w of every tile where there are more than
+// 128 ("both"); otherwise the two groups take turns at the tiles.
+// S_w and P_w share 128 columns of tensor memory, so a group's next scores wait for its second
+// product; the other group's softmax fills that time.
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+    using C = RowsCfg<D>;
+    extern __shared__ __align__(1024) uint8_t ring[];  // all of the block's shared memory
+    if (smem_addr(ring) & 1023u) {  // the swizzle counts on it
+        if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_TIMEOUT, kTag);
+        return;
+    }
+    uint8_t *q_s = ring + C::kStages * C::kStageBytes;
+    uint64_t *kv_full = reinterpret_cast<uint64_t *>(q_s + C::kQBytes), *kv_empty = kv_full + C::kStages;
+    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_done = p_full + 2;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_done + 2);
+    int *first_s = reinterpret_cast<int *>(tmem_ptr + 1);
+    long long *sum_s = reinterpret_cast<long long *>(o_done + 3);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&a.k_map);
+        prefetch_tensormap(&a.v_map);
+        prefetch_tensormap(&a.qp_map);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_ptr, 512);
+        tmem_relinquish();
+    }
+    // rows that no copy fills are zero or an earlier segment's
+    for (int i = tid; i < C::kQBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Deal dealt = deal(a, sum_s, first_s);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_ptr;
+    Walk walk;
+    walk.at = dealt.begin;
+    walk.end = dealt.end;
+    if (walk.at < walk.end) walk.start(a, *first_s, sum_s[kThreads / 32]);
+    Segment s;
+
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0 || warp == 2) {
+        copy_tiles<D, C::kStages>(a, walk, warp ? &a.v_map : &a.k_map, warp ? 1 : 0, ring, kv_full, kv_empty);
+    } else if (warp == 1) {
+        // ------------------------------ Q copies and all products ------------------------------
+        const bool leader = elect_one();
+        int k_st = 0, v_st = 1, seg = 0;
+        uint32_t k_ph = 0, v_ph = 0;
+        int used[2] = {0, 0};  // the groups' second products so far
+        bool ok = true;
+        const uint32_t types = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(128 >> 4) << 24);
+        const uint32_t idesc1 = types | (uint32_t(kTile >> 3) << 17);
+        const uint32_t idesc2 = types | (1u << 16) | (uint32_t(D >> 3) << 17);  // B = V: MN-major
+        // scores of group w, rows from 128 sub on, with the K of the present stage
+        auto first_product = [&](int w, int sub) {
+            if (leader) {
+                const uint64_t qa = sw128_desc(smem_addr(q_s + sub * (128 * 128)));
+                const uint64_t ka = sw128_desc(smem_addr(ring + k_st * C::kStageBytes));
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_f16_ss(tmem + w * 128, qa + (ks / 4) * (C::kRows * 8) + (ks % 4) * 2,
+                                  ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2, idesc1, ks > 0);
+                tc_commit(&s_full[w]);
+            }
+            __syncwarp();
+        };
+        auto wait_k = [&]() {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(&kv_full[k_st], k_ph, a.err, kTag + 7));
+            tc_fence_after();
+            return ok;
+        };
+        auto free_k = [&](bool last) {
+            if (leader) {
+                tc_commit(&kv_empty[k_st]);
+                if (last) tc_commit(q_empty);
+            }
+            __syncwarp();
+            next_turn<C::kStages>(k_st, k_ph);
+        };
+        for (; ok && walk.next(a, s); ++seg) {
+            if (s.t0 == 0 && leader) note_item(a, s, dealt);
+            if (seg > 0)
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(q_empty, uint32_t(seg - 1) & 1u, a.err, kTag + 3));
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(q_full, uint32_t(a.spb * a.share * D * 2));
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(q_s + h * (C::kRows * 128), &a.qp_map, h * 64, s.head * a.share,
+                                s.owner * a.n_seq + s.block * a.spb, q_full);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(q_full, uint32_t(seg) & 1u, a.err, kTag + 6));
+            if (!ok) break;
+            const bool both = s.rows > 128;
+            // the first scores of each group
+            if (!wait_k()) break;
+            first_product(0, 0);
+            if (both) first_product(1, 1);
+            free_k(s.n == 1);
+            if (!both && s.n > 1) {
+                if (!wait_k()) break;
+                first_product(1, 0);
+                free_k(s.n == 2);
+            }
+            for (int i = 0; ok && i < s.n; ++i) {
+                const int keys = s.len - (s.t0 + i) * kTile;
+                const int steps = keys >= kTile ? kTile / 16 : (keys + 15) / 16;
+                for (int w = both ? 0 : i & 1; w <= (both ? 1 : i & 1); ++w) {
+                    const bool got = mbar_wait_spin(&kv_full[v_st], v_ph, a.err, kTag + 4) &&
+                                     mbar_wait_spin(&p_full[w], uint32_t(used[w]) & 1u, a.err, kTag + 5);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    ++used[w];
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t va = smem_desc(smem_addr(ring + v_st * C::kStageBytes),
+                                                      C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
+                        const bool add = i >= (both ? 1 : 2);
+                        // (16 keys are 8 columns of P, and 2048 bytes of V: 128 units of the address)
+                        for (int ks = 0; ks < steps; ++ks)
+                            tc_mma_f16_ta(tmem + C::kOCol + w * 128, tmem + w * 128 + ks * 8, va + ks * 128,
+                                          idesc2, add || ks > 0);
+                        tc_commit(&o_done[w]);
+                        if (!both || w == 1) tc_commit(&kv_empty[v_st]);
+                    }
+                    __syncwarp();
+                    // the group's next scores, over its weights (products run in order)
+                    if (i + (both ? 1 : 2) < s.n) {
+                        if (!both || w == 0) {
+                            if (!wait_k()) break;
+                        }
+                        first_product(w, both ? w : 0);
+                        if (!both || w == 1) free_k(i + (both ? 1 : 2) == s.n - 1);
+                    }
+                }
+                next_turn<C::kStages>(v_st, v_ph);
+            }
+        }
+        // the products in flight end before tensor memory is freed: the softmax warps' wait for this
+        // one runs out after them
+        if (!ok && leader) tc_commit(&o_done[0]);
+    } else if (warp >= 4) {
+        // ---------------------------------- softmax: thread = row ----------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        const int w = warp >= 8;  // group
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + C::kOCol + w * 128;
+        const float2 scale = make_float2(a.scale_log2, a.scale_log2);
+        int done = 0;  // the group's tiles so far
+        int st = 1;    // the ring stage of the tile's V
+        uint32_t ph = 0;
+        bool dead = false;  // as in attn_kernel
+        auto wait = [&](uint64_t *bar, int use, int tag) {
+            if (!dead)
+                dead = !__all_sync(0xffffffffu, mbar_wait_spin(bar, uint32_t(use) & 1u, a.err, tag));
+        };
+        while (walk.next(a, s)) {
+            const bool both = s.rows > 128;
+            float nref = 0.0f, l = 0.0f;  // kLift - ref, sum
+            bool fresh = true;
+            for (int i = 0; i < s.n; ++i) {
+                const int v_st = st;
+                const uint32_t v_ph = ph;
+                next_turn<C::kStages>(st, ph);
+                if (!both && (i & 1) != w) continue;
+                const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
+                wait(&s_full[w], done, kTag + 9);
+                tc_fence_after();
+                float v[kTile];
+                {
+                    uint32_t r[kTile];
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) tmem_ld32_issue(s_col + c, r + c);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < kTile; j += 2)
+                        *reinterpret_cast<float2 *>(v + j) =
+                            fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), scale,
+                                 make_float2(0.0f, 0.0f));
+                }
+                if (keys < kTile) {
+#pragma unroll
+                    for (int j = 0; j < kTile; ++j) v[j] = j < keys ? v[j] : -INFINITY;
+                }
+                float most[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    most[e] = v[e];
+#pragma unroll
+                    for (int j = 4; j < kTile - 4; j += 8) most[e] = max3(most[e], v[j + e], v[j + 4 + e]);
+                    most[e] = fmaxf(most[e], v[kTile - 4 + e]);
+                }
+                most[0] = fmaxf(max3(most[0], most[1], most[2]), most[3]);
+                const bool raise = fresh || most[0] + nref > kSlack + kLift;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float old = fresh ? -INFINITY : kLift - nref;
+                    // no key counts (scores of -inf): any finite reference does
+                    const float ref = raise ? fmaxf(fmaxf(most[0], old), -1e30f) : old;
+                    const float f = fresh ? 0.0f : ex2(old - ref);
+                    nref = kLift - ref;
+                    l *= f;
+                    if (!fresh) {  // the products into this output so far are done
+                        wait(&o_done[w], done - 1, kTag + 14);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            tmem_load<16>(o_col + c, o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] *= f;
+                            tmem_store<16>(o_col + c, o);
+                        }
+                    }
+                }
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                const float2 off = make_float2(nref, nref);
+#pragma unroll
+                for (int c = 0; c < kTile; c += 64) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        float2 e = add2(make_float2(v[c + j], v[c + j + 1]), off);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        sum[j / 2 & 1] = add2(sum[j / 2 & 1], e);
+                        p[j / 2] = pack<BF>(e.x, e.y);
+                    }
+                    tmem_st32(s_col + c / 2, p);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                if (keys < kTile && (keys & 15) && (!both || w == 0)) {
+                    // places past the last key up to the product's 16: whatever V holds there,
+                    // 0 times it has to be 0
+                    wait(&kv_full[v_st], int(v_ph), kTag + 12);
+                    const int n0 = 16 - (keys & 15);
+                    for (int x = row; x < n0 * C::kHalves * 8; x += 128) {
+                        const int piece = x & 7, r = (x >> 3) / C::kHalves, h = (x >> 3) % C::kHalves;
+                        *reinterpret_cast<uint4 *>(ring + v_st * C::kStageBytes + h * (kTile * 128) +
+                                                   (keys + r) * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[w]);
+                fresh = false;
+                ++done;
+            }
+            // ---- the segment's output, reference and sum
+            const int rows = both ? s.rows - 128 * w : s.rows;  // of the group
+            const int64_t at = (record_of(a, s) + w) * 128 + row;
+            if (row < rows) a.p_ml[at] = fresh ? make_float2(-1e30f, 0.0f) : make_float2(kLift - nref, l);
+            if (fresh) continue;
+            wait(&o_done[w], done - 1, kTag + 13);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_load<32>(o_col + c, o);
+                if (row < rows) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(a.p_out + at * D + c + j) =
+                            make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // Joins the records of each query row: `split` warps of a block to a row, each with every
 // split-th record; their sums meet in shared memory.
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int ncap,
-                                                        int split) {
+                                                        int split, int by_rows) {
     constexpr int E = D / 32;  // elements per lane
     __shared__ float s_m[8], s_l[8];
     __shared__ float s_o[8][D];
@@ -858,6 +1190,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         int2 pi = make_int2(0, 0), si = make_int2(0, 0);
         if (plen) pi = __ldcg(a.p_item + (int64_t(group) * a.n_kv + head) * a.row_blocks + block);
         if (slen) si = __ldcg(a.s_item + int64_t(b) * a.n_kv + head);
+        // of a prefix block of more than 128 rows, a segment's two records are those of different rows
+        const int seqs = min(a.spb, a.n_seq - block * a.spb);
+        const bool both = by_rows && seqs * a.share > 128;
+        const int pstep = both ? 2 : 1, prow = both ? pr & 127 : pr;
+        if (both) {
+            pi.x += pr >> 7;
+            pi.y >>= 1;
+        }
         const int np = pi.y, n = np + si.y;
         // 32 records at a time: lane i has the i-th's reference and sum
         for (int i0 = part; i0 < n; i0 += 32 * split) {
@@ -865,7 +1205,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
             float2 ml = make_float2(-INFINITY, 0.0f);
             const float *o = nullptr;
             if (i < n) {
-                const int64_t x = i < np ? (int64_t(pi.x) + i) * ncap + pr
+                const int64_t x = i < np ? (int64_t(pi.x) + i * pstep) * ncap + prow
                                          : (int64_t(si.x) + i - np) * a.share + r;
                 ml = __ldcg((i < np ? a.p_ml : a.s_ml) + x);
                 o = (i < np ? a.p_out : a.s_out) + x * D;
@@ -944,6 +1284,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 struct q2_0_attn_plan {
     q2::AttnArgs args;
     int ncap, dim, n_layers;
+    bool by_rows;  // prefixes by attn_rows_kernel
     bool bf;
     int64_t n_pages;
     void *scratch;
@@ -970,9 +1311,15 @@ Variant variant_n(int dim, bool bf) {
     return bf ? variant<NCAP, 128, true>() : variant<NCAP, 128, false>();
 }
 Variant variant_of(int ncap, int dim, bool bf) {
-    if (ncap == 32) return variant_n<32>(dim, bf);
-    if (ncap == 64) return variant_n<64>(dim, bf);
-    return variant_n<128>(dim, bf);
+    return ncap == 32 ? variant_n<32>(dim, bf) : variant_n<64>(dim, bf);
+}
+template <int D, bool BF>
+Variant rows_variant() {
+    return {attn_rows_kernel<D, BF>, RowsCfg<D>::kSmem};
+}
+Variant rows_variant_of(int dim, bool bf) {
+    if (dim == 64) return bf ? rows_variant<64, true>() : rows_variant<64, false>();
+    return bf ? rows_variant<128, true>() : rows_variant<128, false>();
 }
 
 }  // namespace
@@ -999,15 +1346,15 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     a.n_kv = c.n_kv;
     a.share = d.n_q / c.n_kv;
     a.page_shift = log2_of(c.page);
-    a.dim = c.dim;
     a.row0 = 0;
     a.scale_log2 = d.scale * 1.44269504f;
     a.grid = sms;
     a.err = err;
-    // the smallest product that holds a prefix's rows: 32, 64 or 128 at a time
+    // More than 64 rows to a prefix: 256 at a time by attn_rows_kernel.
     const int64_t rows = d.prefix_width ? d.n_seq * a.share : a.share;
-    p->ncap = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    a.spb = int(std::min<int64_t>(d.n_seq, p->ncap / a.share));
+    p->by_rows = d.prefix_width && rows > 64;
+    p->ncap = (p->by_rows ? a.share : rows) <= 32 ? 32 : 64;
+    a.spb = int(std::min<int64_t>(d.n_seq, (p->by_rows ? 256 : p->ncap) / a.share));
     a.row_blocks = d.prefix_width ? (a.n_seq + a.spb - 1) / a.spb : 1;
     p->dim = c.dim;
     p->n_layers = c.n_layers;
@@ -1041,15 +1388,18 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     };
     const size_t o_pi = take(size_t(a.n_groups) * a.n_kv * a.row_blocks * 8);
     const size_t o_si = take(size_t(seqs) * a.n_kv * 8);
-    const size_t recs = p->ncap <= 64 ? 2 : 1;
-    const size_t o_p = take(recs * p_slots * p->ncap * c.dim * 4);
-    const size_t o_s = take(recs * s_slots * a.share * c.dim * 4);
-    const size_t o_pml = take(recs * p_slots * p->ncap * 8), o_sml = take(recs * s_slots * a.share * 8);
+    const size_t p_rows = 2 * p_slots * (p->by_rows ? 128 : p->ncap), s_rows = 2 * s_slots * a.share;
+    const size_t o_p = take(p_rows * c.dim * 4), o_s = take(s_rows * c.dim * 4);
+    const size_t o_pml = take(p_rows * 8), o_sml = take(s_rows * 8);
     p->scratch = nullptr;
     if (ok) ok = cudaMalloc(&p->scratch, at) == cudaSuccess;
     const Variant v = variant_of(p->ncap, p->dim, p->bf);
     if (ok)
         ok = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) ==
+             cudaSuccess;
+    const Variant vr = rows_variant_of(p->dim, p->bf);
+    if (ok && p->by_rows)
+        ok = cudaFuncSetAttribute(vr.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, vr.smem) ==
              cudaSuccess;
     if (!ok) {
         if (p->scratch) cudaFree(p->scratch);
@@ -1082,8 +1432,21 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(unsigned(a.grid));
     cfg.blockDim = dim3(kThreads);
+    cudaError_t e;
+    const int owners = a.n_groups + a.n_groups * a.n_seq;
+    a.own0 = 0;
+    a.own1 = owners;
+    if (p->by_rows) {
+        const Variant vr = rows_variant_of(p->dim, p->bf);
+        a.own1 = a.n_groups;
+        cfg.dynamicSmemBytes = size_t(vr.smem);
+        e = cudaLaunchKernelEx(&cfg, vr.fn, a);
+        if (e != cudaSuccess) return cuda_status(e);
+        a.own0 = a.n_groups;
+        a.own1 = owners;
+    }
     cfg.dynamicSmemBytes = size_t(v.smem);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, a);
+    e = cudaLaunchKernelEx(&cfg, v.fn, a);
     if (e != cudaSuccess) return cuda_status(e);
     // few rows have many records each: more warps to a row
     const int64_t rows = int64_t(a.n_groups) * a.n_seq * a.n_q;
@@ -1093,10 +1456,10 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     cfg.dynamicSmemBytes = 0;
     auto *join = p->dim == 64 ? (p->bf ? attn_join_kernel<64, true> : attn_join_kernel<64, false>)
                               : (p->bf ? attn_join_kernel<128, true> : attn_join_kernel<128, false>);
-    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->ncap, split));
+    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->by_rows ? 128 : p->ncap, split, int(p->by_rows)));
 }
 
-int attn_plan_launches(const q2_0_attn_plan *) { return 2; }
+int attn_plan_launches(const q2_0_attn_plan *p) { return p->by_rows ? 3 : 2; }
 
 int attn_plan_layers(const q2_0_attn_plan *p) { return p->n_layers; }
 
