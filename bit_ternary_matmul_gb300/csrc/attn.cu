@@ -49,9 +49,10 @@ namespace {
 
 constexpr int kTile = 128;     // keys per tile
 constexpr int kThreads = 384;  // 4 warps that copy and multiply, 8 of softmax
-// Registers: launched with 168 per thread (64512), the first four warps leave with 88, so that
-// the softmax warps hold 128 scores: 128 * 88 + 256 * 208 = 64512.
-constexpr int kRegsFew = 88, kRegsMany = 208;
+// Registers: launched with 168 per thread, 64512 in all; the first four warps leave some (kRegsFew)
+// to the softmax warps (kRegsMany). A spilled register costs more here than elsewhere: shared
+// memory leaves the first-level cache next to nothing.
+constexpr bool regs_fit(int few, int many) { return 128 * few + 256 * many == 384 * 168; }
 constexpr int kTag = 300;      // waits' tags: 301..
 constexpr float kLift = 7.0f;  // p = 2^(s - ref + kLift)
 constexpr float kSlack = 8.0f; // how far a score may pass the reference
@@ -61,6 +62,8 @@ constexpr int kTileCost = 4, kItemCost = 4;
 // Sizes of a variant of attn_kernel: NCAP, 32 or 64, is the most query rows of a product.
 template <int NCAP, int D>
 struct Cfg {
+    static constexpr int kRegsFew = NCAP == 32 ? 136 : 88, kRegsMany = NCAP == 32 ? 184 : 208;
+    static_assert(regs_fit(kRegsFew, kRegsMany), "registers");
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kHalves = D / 64;
     static constexpr int kQBufs = NCAP <= 32 ? 2 : 1;
@@ -69,31 +72,36 @@ struct Cfg {
     static constexpr int kRefs = 2 * 5 * NCAP;  // floats
     // references, barriers, the tile list's 12 + 2 sums
     static constexpr int kSmall = kRefs * 4 + 448;
-    // An even number: K and V then have stages of their own. (Their consumers are different warps;
+    // K and V have stages of their own, half of the ring each. (Their consumers are different warps;
     // in a shared stage one could be a whole phase ahead of the other, which a wait by parity
-    // does not see.)
+    // does not see.) A fifth stage of NCAP = 64, D = 128, given to either, was slower (60 against
+    // 55.5 us for 64 rows and 50021 keys).
     static constexpr int kStages =
         (227 * 1024 - kSmall - kQBufs * kQBytes - 2 * kPBytes) / kStageBytes / 2 * 2;
+    static constexpr int kK = kStages / 2, kV = kK;
     static constexpr int kTmemCols = 4 * NCAP;
     static constexpr int kOCol = 2 * NCAP;  // S buffers at 0 and NCAP, O at 2 NCAP and 3 NCAP
     static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes;
     static constexpr int kBars = 2 * kStages + 2 * kQBufs + 10;
-    static_assert(kStages >= 4 && kStages % 2 == 0 && kSmem <= 227 * 1024, "shared memory");
+    static_assert(kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
     static_assert((kBars + 1 + kThreads / 32 + 2) * 8 <= 448, "barriers and sums");
 };
 
-// Sizes of attn_rows_kernel: 256 query rows of D, two sub-blocks of 128.
-template <int D>
+// Sizes of attn_rows_kernel: kRows, 128 or 256, query rows of D.
+template <int ROWS, int D>
 struct RowsCfg {
-    static constexpr int kRows = 256;
+    static constexpr int kRows = ROWS;
+    static constexpr int kRegsFew = 120, kRegsMany = 192;
+    static_assert(regs_fit(kRegsFew, kRegsMany), "registers");
     static constexpr int kStageBytes = kTile * D * 2;
     static constexpr int kHalves = D / 64;
     static constexpr int kQBytes = kRows * D * 2;
-    static constexpr int kSmall = 448;
-    static constexpr int kStages = (227 * 1024 - kSmall - kQBytes) / kStageBytes / 2 * 2;  // even, as above
+    static constexpr int kSmall = 512;
+    static constexpr int kStages = (227 * 1024 - kSmall - kQBytes) / kStageBytes;
+    static constexpr int kK = kStages / 2, kV = kStages - kK;  // as above
     static constexpr int kOCol = 256;  // S (and P) at 0 and 128, O at 256 and 384
     static constexpr int kSmem = kSmall + kStages * kStageBytes + kQBytes;
-    static constexpr int kBars = 2 * kStages + 2 + 6;
+    static constexpr int kBars = 2 * kStages + 2 + 8;
     static_assert(kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
     static_assert((kBars + 1 + kThreads / 32 + 2) * 8 <= kSmall, "barriers and sums");
 };
@@ -345,11 +353,11 @@ __device__ __forceinline__ void with_columns(int cols, F f) {
     }
 }
 
-// K and V alternate in a ring: from a stage to the next of its kind.
-template <int kStages>
-__device__ __forceinline__ void next_turn(int &st, uint32_t &ph) {
-    if ((st += 2) >= kStages) {
-        st -= kStages;
+// From a stage of a ring of kN to the next.
+template <int kN>
+__device__ __forceinline__ void next_stage(int &st, uint32_t &ph) {
+    if (++st == kN) {
+        st = 0;
         ph ^= 1u;
     }
 }
@@ -404,11 +412,11 @@ __device__ __forceinline__ Deal deal(const AttnArgs &a, long long *sum_s, int *f
     return {T, begin, end, G};
 }
 
-// The warp's copies of K or V of the block's tiles, into every second stage of the ring from
-// `first` on. K and V have a warp each: with short pages the issue of a tile's copies takes
+// The warp's copies of K or V of the block's tiles, into their ring. K and V have a
+// warp each: with short pages the issue of a tile's copies takes
 // longer than they do.
-template <int D, int kStages>
-__device__ __forceinline__ void copy_tiles(const AttnArgs &a, Walk walk, const CUtensorMap *map, int first,
+template <int D>
+__device__ __forceinline__ void copy_tiles(const AttnArgs &a, Walk walk, const CUtensorMap *map, int stages,
                                            uint8_t *ring, uint64_t *kv_full, uint64_t *kv_empty) {
     constexpr int kHalves = D / 64, kStageBytes = kTile * D * 2;
     const int lane = threadIdx.x & 31;
@@ -416,7 +424,7 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs &a, Walk walk, const C
     const int page = 1 << a.page_shift;
     const int box = page < kTile ? page : kTile;
     const int box_bytes = box * 128;
-    int st = first;
+    int st = 0;
     uint32_t ph = 0;
     bool ok = true;
     while (ok && walk.next(a, s)) {
@@ -455,13 +463,16 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs &a, Walk walk, const C
             if (b < n)
                 tma_load_2d(ring + st * kStageBytes + half * (kTile * 128) + b * box_bytes, map,
                             half * 64, at, &kv_full[st]);
-            next_turn<kStages>(st, ph);
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
         }
     }
     if (!ok)  // let the copies in flight land (bounded)
-        for (int k = 0; k < kStages / 2; ++k) {
-            if ((st -= 2) < 0) {
-                st += kStages;
+        for (int k = 0; k < stages; ++k) {
+            if (--st < 0) {
+                st = stages - 1;
                 ph ^= 1u;
             }
             mbar_wait(&kv_full[st], ph, a.err, kTag + 2);
@@ -497,8 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
     float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 5 NCAP]
     uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kRefs);
-    uint64_t *kv_full = bars, *kv_empty = kv_full + C::kStages;
-    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + C::kQBufs;
+    uint8_t *v_ring = ring + C::kK * C::kStageBytes;
+    uint64_t *k_full = bars, *k_empty = k_full + C::kK;
+    uint64_t *v_full = k_empty + C::kK, *v_empty = v_full + C::kV;
+    uint64_t *q_full = v_empty + C::kV, *q_empty = q_full + C::kQBufs;
     uint64_t *s_full = q_empty + C::kQBufs, *s_empty = s_full + 2;
     uint64_t *p_full = s_empty + 2, *p_empty = p_full + 2;
     uint64_t *o_full = p_empty + 2;
@@ -508,10 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
-        }
+        for (int i = 0; i < 2 * C::kStages; ++i) mbar_init(&k_full[i], 1);  // the four rings of barriers
         for (int i = 0; i < C::kQBufs; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -552,10 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     walk.end = dealt.end;
     if (walk.at < walk.end) walk.start(a, *first_s, sum_s[kThreads / 32]);
     Segment s;
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFew));
     if (warp == 0 || warp == 2) {
         // ------------------------- K (warp 0) and V (warp 2) copies -------------------------
-        copy_tiles<D, C::kStages>(a, walk, warp ? &a.v_map : &a.k_map, warp ? 1 : 0, ring, kv_full, kv_empty);
+        copy_tiles<D>(a, walk, warp ? &a.v_map : &a.k_map, warp ? C::kV : C::kK, warp ? v_ring : ring,
+                      warp ? v_full : k_full, warp ? v_empty : k_empty);
     } else if (warp == 1) {
         // ----------------------- Q copies and the first products -----------------------
         const bool leader = elect_one();
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 const int sb = n & 1;
                 const uint32_t use = uint32_t(n >> 1);
                 bool got = use == 0 || mbar_wait_spin(&s_empty[sb], (use - 1) & 1u, a.err, kTag + 8);
-                got = got && mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 7);
+                got = got && mbar_wait_spin(&k_full[st], ph, a.err, kTag + 7);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
@@ -609,18 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         tc_mma_f16_ss(tmem + sb * NCAP, ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2,
                                       qa + (ks / 4) * (NCAP * 8) + (ks % 4) * 2, idesc, ks > 0);
                     tc_commit(&s_full[sb]);
-                    tc_commit(&kv_empty[st]);
+                    tc_commit(&k_empty[st]);
                     if (i == s.n - 1) tc_commit(&q_empty[qb]);
                 }
                 __syncwarp();
-                next_turn<C::kStages>(st, ph);
+                next_stage<C::kK>(st, ph);
             }
             if (C::kQBufs == 1 && ok && more) ok = load_q(ahead, seg + 1);
         }
     } else if (warp == 3) {
         // ------------------------------- the second products -------------------------------
         const bool leader = elect_one();
-        int st = 1;
+        int st = 0;
         uint32_t ph = 0;
         int n = 0;  // tiles so far
         bool ok = true;
@@ -632,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int pb = n & 1;
                 const int keys = s.len - (s.t0 + i) * kTile;
-                const bool got = mbar_wait_spin(&kv_full[st], ph, a.err, kTag + 4) &&
+                const bool got = mbar_wait_spin(&v_full[st], ph, a.err, kTag + 4) &&
                                  mbar_wait_spin(&p_full[pb], uint32_t(n >> 1) & 1u, a.err, kTag + 5);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint64_t va = smem_desc(smem_addr(ring + st * C::kStageBytes),
+                    const uint64_t va = smem_desc(smem_addr(v_ring + st * C::kStageBytes),
                                                   C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
                     const uint64_t pa = smem_desc(smem_addr(p_s + pb * C::kPBytes), 128, kTile * 16, 0);
                     const uint32_t o = tmem + C::kOCol + pb * NCAP;
@@ -653,11 +664,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             tc_mma_f16_ss(o, va + ks * 128, pa + ks * 16, idesc, add || ks > 0);
                     }
                     tc_commit(&p_empty[pb]);
-                    tc_commit(&kv_empty[st]);
+                    tc_commit(&v_empty[st]);
                     if (i >= s.n - 2) tc_commit(&o_full[pb]);
                 }
                 __syncwarp();
-                next_turn<C::kStages>(st, ph);
+                next_stage<C::kV>(st, ph);
             }
         }
         // the products in flight end before tensor memory is freed: the softmax warps' wait for this
@@ -666,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     } else if (warp >= 4) {
         // ---------------------------------- softmax ----------------------------------
         // Thread = key `key` of the tile, or element `key` of the head in the output.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsMany));
         const int w = warp >= 8;  // group
         const int quarter = warp & 3;
         const int key = quarter * 32 + lane;
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         float2 l[NCAP / 2];
         int n = 0;         // tiles so far
         int segs = 0;      // the group's segments so far
-        int st = 1;        // the ring stage of the tile's V
+        int st = 0;        // the stage of the tile's V
         uint32_t ph = 0;
         // A warp whose wait timed out waits no more: it goes through the motions, so that
         // the barriers of the softmax warps stay matched, and its results mean nothing.
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             for (int i = 0; i < s.n; ++i, ++n) {
                 const int v_st = st;
                 const uint32_t v_ph = ph;
-                next_turn<C::kStages>(st, ph);
+                next_stage<C::kV>(st, ph);
                 if ((n & 1) != w) continue;
                 // (the group's buffers of scores, weights and outputs are number w)
                 const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
@@ -809,11 +820,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 if (keys < kTile && (keys & 15)) {
                     // places past the last key up to the product's 16: whatever V holds there,
                     // 0 times it has to be 0
-                    wait(&kv_full[v_st], int(v_ph), kTag + 12);
+                    wait(&v_full[v_st], int(v_ph), kTag + 12);
                     const int n0 = 16 - (keys & 15);
                     for (int x = key; x < n0 * C::kHalves * 8; x += 128) {
                         const int piece = x & 7, r = (x >> 3) / C::kHalves, h = (x >> 3) % C::kHalves;
-                        *reinterpret_cast<uint4 *>(ring + v_st * C::kStageBytes + h * (kTile * 128) +
+                        *reinterpret_cast<uint4 *>(v_ring + v_st * C::kStageBytes + h * (kTile * 128) +
                                                    (keys + r) * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
@@ -869,34 +880,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // rows, softmax group w has rows 128 w .. 127 + 128 w of every tile where there are more than
 // 128 ("both"); otherwise the two groups take turns at the tiles.
 // S_w and P_w share 128 columns of tensor memory, so a group's next scores wait for its second
-// product; the other group's softmax fills that time.
-template <int D, bool BF>
+// product; the other group's softmax fills that time, and the weights are handed over in
+// halves of 64 keys. (Scores in halves, too, would cost more than they save: a product of N =
+// 64 reads as much of Q from shared memory as one of 128, and takes as long.) A product step holds its issuing warp
+// about as long as it runs, so that the two kinds have a warp each.
+template <int ROWS, int D, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
-    using C = RowsCfg<D>;
+    using C = RowsCfg<ROWS, D>;
     extern __shared__ __align__(1024) uint8_t ring[];  // all of the block's shared memory
     if (smem_addr(ring) & 1023u) {  // the swizzle counts on it
         if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_TIMEOUT, kTag);
         return;
     }
     uint8_t *q_s = ring + C::kStages * C::kStageBytes;
-    uint64_t *kv_full = reinterpret_cast<uint64_t *>(q_s + C::kQBytes), *kv_empty = kv_full + C::kStages;
-    uint64_t *q_full = kv_empty + C::kStages, *q_empty = q_full + 1;
-    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_done = p_full + 2;
+    uint8_t *v_ring = ring + C::kK * C::kStageBytes;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(q_s + C::kQBytes), *k_empty = k_full + C::kK;
+    uint64_t *v_full = k_empty + C::kK, *v_empty = v_full + C::kV;
+    uint64_t *q_full = v_empty + C::kV, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_done = p_full + 4;  // p_full: 2 w + half
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(o_done + 2);
     int *first_s = reinterpret_cast<int *>(tmem_ptr + 1);
     long long *sum_s = reinterpret_cast<long long *>(o_done + 3);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
-        }
+        for (int i = 0; i < 2 * C::kStages; ++i) mbar_init(&k_full[i], 1);  // the four rings of barriers
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_done[i], 1);
         }
         fence_barrier_init();
@@ -925,45 +939,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
     if (walk.at < walk.end) walk.start(a, *first_s, sum_s[kThreads / 32]);
     Segment s;
 
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFew));
     if (warp == 0 || warp == 2) {
-        copy_tiles<D, C::kStages>(a, walk, warp ? &a.v_map : &a.k_map, warp ? 1 : 0, ring, kv_full, kv_empty);
+        copy_tiles<D>(a, walk, warp ? &a.v_map : &a.k_map, warp ? C::kV : C::kK, warp ? v_ring : ring,
+                      warp ? v_full : k_full, warp ? v_empty : k_empty);
     } else if (warp == 1) {
-        // ------------------------------ Q copies and all products ------------------------------
+        // ----------------------- Q copies and the first products -----------------------
         const bool leader = elect_one();
-        int k_st = 0, v_st = 1, seg = 0;
-        uint32_t k_ph = 0, v_ph = 0;
-        int used[2] = {0, 0};  // the groups' second products so far
+        int st = 0, seg = 0;
+        uint32_t ph = 0;
+        int count[2] = {0, 0};  // the groups' tiles so far
         bool ok = true;
-        const uint32_t types = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(128 >> 4) << 24);
-        const uint32_t idesc1 = types | (uint32_t(kTile >> 3) << 17);
-        const uint32_t idesc2 = types | (1u << 16) | (uint32_t(D >> 3) << 17);  // B = V: MN-major
-        // scores of group w, rows from 128 sub on, with the K of the present stage
-        auto first_product = [&](int w, int sub) {
-            if (leader) {
-                const uint64_t qa = sw128_desc(smem_addr(q_s + sub * (128 * 128)));
-                const uint64_t ka = sw128_desc(smem_addr(ring + k_st * C::kStageBytes));
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma_f16_ss(tmem + w * 128, qa + (ks / 4) * (C::kRows * 8) + (ks % 4) * 2,
-                                  ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2, idesc1, ks > 0);
-                tc_commit(&s_full[w]);
-            }
-            __syncwarp();
-        };
-        auto wait_k = [&]() {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(&kv_full[k_st], k_ph, a.err, kTag + 7));
-            tc_fence_after();
-            return ok;
-        };
-        auto free_k = [&](bool last) {
-            if (leader) {
-                tc_commit(&kv_empty[k_st]);
-                if (last) tc_commit(q_empty);
-            }
-            __syncwarp();
-            next_turn<C::kStages>(k_st, k_ph);
-        };
+        const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(kTile >> 3) << 17) |
+                               (uint32_t(128 >> 4) << 24);
         for (; ok && walk.next(a, s); ++seg) {
             if (s.t0 == 0 && leader) note_item(a, s, dealt);
             if (seg > 0)
@@ -977,50 +965,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
             }
             __syncwarp();
             ok = __all_sync(0xffffffffu, mbar_wait_spin(q_full, uint32_t(seg) & 1u, a.err, kTag + 6));
-            if (!ok) break;
-            const bool both = s.rows > 128;
-            // the first scores of each group
-            if (!wait_k()) break;
-            first_product(0, 0);
-            if (both) first_product(1, 1);
-            free_k(s.n == 1);
-            if (!both && s.n > 1) {
-                if (!wait_k()) break;
-                first_product(1, 0);
-                free_k(s.n == 2);
+            const bool both = ROWS > 128 && s.rows > 128;
+            for (int i = 0; ok && i < s.n; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(&k_full[st], ph, a.err, kTag + 7));
+                const uint64_t ka = sw128_desc(smem_addr(ring + st * C::kStageBytes));
+                const int w0 = both ? 0 : i & 1, w1 = both ? 1 : i & 1;
+                for (int w = w0; ok && w <= w1; ++w) {
+                    // the scores' place held the weights of the group's tile before
+                    if (count[w] > 0)
+                        ok = __all_sync(0xffffffffu, mbar_wait_spin(&o_done[w], uint32_t(count[w] - 1) & 1u,
+                                                                    a.err, kTag + 8));
+                    if (!ok) break;
+                    ++count[w];
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t qa = sw128_desc(smem_addr(q_s + (both ? w : 0) * (128 * 128)));
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            tc_mma_f16_ss(tmem + w * 128, qa + (ks / 4) * (C::kRows * 8) + (ks % 4) * 2,
+                                          ka + (ks / 4) * (kTile * 8) + (ks % 4) * 2, idesc, ks > 0);
+                        tc_commit(&s_full[w]);
+                        if (w == w1) tc_commit(&k_empty[st]);
+                        if (w == w1 && i == s.n - 1) tc_commit(q_empty);
+                    }
+                    __syncwarp();
+                }
+                next_stage<C::kK>(st, ph);
             }
+        }
+    } else if (warp == 3) {
+        // ------------------------------- the second products -------------------------------
+        const bool leader = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        int count[2] = {0, 0};
+        bool ok = true;
+        // B = V: MN-major
+        const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (1u << 16) |
+                               (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+        while (ok && walk.next(a, s)) {
+            const bool both = ROWS > 128 && s.rows > 128;
             for (int i = 0; ok && i < s.n; ++i) {
                 const int keys = s.len - (s.t0 + i) * kTile;
                 const int steps = keys >= kTile ? kTile / 16 : (keys + 15) / 16;
-                for (int w = both ? 0 : i & 1; w <= (both ? 1 : i & 1); ++w) {
-                    const bool got = mbar_wait_spin(&kv_full[v_st], v_ph, a.err, kTag + 4) &&
-                                     mbar_wait_spin(&p_full[w], uint32_t(used[w]) & 1u, a.err, kTag + 5);
-                    ok = __all_sync(0xffffffffu, got);
-                    if (!ok) break;
-                    ++used[w];
-                    tc_fence_after();
-                    if (leader) {
-                        const uint64_t va = smem_desc(smem_addr(ring + v_st * C::kStageBytes),
-                                                      C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
-                        const bool add = i >= (both ? 1 : 2);
-                        // (16 keys are 8 columns of P, and 2048 bytes of V: 128 units of the address)
-                        for (int ks = 0; ks < steps; ++ks)
-                            tc_mma_f16_ta(tmem + C::kOCol + w * 128, tmem + w * 128 + ks * 8, va + ks * 128,
-                                          idesc2, add || ks > 0);
-                        tc_commit(&o_done[w]);
-                        if (!both || w == 1) tc_commit(&kv_empty[v_st]);
-                    }
-                    __syncwarp();
-                    // the group's next scores, over its weights (products run in order)
-                    if (i + (both ? 1 : 2) < s.n) {
-                        if (!both || w == 0) {
-                            if (!wait_k()) break;
+                const int w0 = both ? 0 : i & 1, w1 = both ? 1 : i & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(&v_full[st], ph, a.err, kTag + 4));
+                const uint64_t va = smem_desc(smem_addr(v_ring + st * C::kStageBytes),
+                                              C::kHalves == 2 ? kTile * 128 : 0, 1024, 2);
+                const bool add = i >= (both ? 1 : 2);  // not the output's first
+                for (int w = w0; ok && w <= w1; ++w) {
+                    for (int hf = 0; ok && hf < 2; ++hf) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_spin(&p_full[2 * w + hf], uint32_t(count[w]) & 1u,
+                                                                    a.err, kTag + 5));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            // (16 keys are 8 columns of P, and 2048 bytes of V: 128 units of the address)
+                            for (int ks = 4 * hf; ks < min(4 * hf + 4, steps); ++ks)
+                                tc_mma_f16_ta(tmem + C::kOCol + w * 128, tmem + w * 128 + ks * 8, va + ks * 128,
+                                              idesc, add || ks > 0);
+                            if (hf) tc_commit(&o_done[w]);
+                            if (hf && w == w1) tc_commit(&v_empty[st]);
                         }
-                        first_product(w, both ? w : 0);
-                        if (!both || w == 1) free_k(i + (both ? 1 : 2) == s.n - 1);
+                        __syncwarp();
                     }
+                    ++count[w];
                 }
-                next_turn<C::kStages>(v_st, v_ph);
+                next_stage<C::kV>(st, ph);
             }
         }
         // the products in flight end before tensor memory is freed: the softmax warps' wait for this
@@ -1028,14 +1039,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
         if (!ok && leader) tc_commit(&o_done[0]);
     } else if (warp >= 4) {
         // ---------------------------------- softmax: thread = row ----------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsMany));
         const int w = warp >= 8;  // group
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + C::kOCol + w * 128;
         const float2 scale = make_float2(a.scale_log2, a.scale_log2);
         int done = 0;  // the group's tiles so far
-        int st = 1;    // the ring stage of the tile's V
+        int st = 0;    // the stage of the tile's V
         uint32_t ph = 0;
         bool dead = false;  // as in attn_kernel
         auto wait = [&](uint64_t *bar, int use, int tag) {
@@ -1043,13 +1054,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                 dead = !__all_sync(0xffffffffu, mbar_wait_spin(bar, uint32_t(use) & 1u, a.err, tag));
         };
         while (walk.next(a, s)) {
-            const bool both = s.rows > 128;
+            const bool both = ROWS > 128 && s.rows > 128;
             float nref = 0.0f, l = 0.0f;  // kLift - ref, sum
             bool fresh = true;
             for (int i = 0; i < s.n; ++i) {
                 const int v_st = st;
                 const uint32_t v_ph = ph;
-                next_turn<C::kStages>(st, ph);
+                next_stage<C::kV>(st, ph);
                 if (!both && (i & 1) != w) continue;
                 const int keys = s.len - (s.t0 + i) * kTile;  // valid ones of this tile, if < 128
                 wait(&s_full[w], done, kTag + 9);
@@ -1100,6 +1111,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                         }
                     }
                 }
+                if (keys < kTile && (keys & 15) && (!both || w == 0)) {
+                    // places past the last key up to the product's 16: whatever V holds there,
+                    // 0 times it has to be 0
+                    wait(&v_full[v_st], int(v_ph), kTag + 12);
+                    const int n0 = 16 - (keys & 15);
+                    for (int x = row; x < n0 * C::kHalves * 8; x += 128) {
+                        const int piece = x & 7, r = (x >> 3) / C::kHalves, h = (x >> 3) % C::kHalves;
+                        *reinterpret_cast<uint4 *>(v_ring + v_st * C::kStageBytes + h * (kTile * 128) +
+                                                   (keys + r) * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 const float2 off = make_float2(nref, nref);
 #pragma unroll
@@ -1114,24 +1137,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                         p[j / 2] = pack<BF>(e.x, e.y);
                     }
                     tmem_st32(s_col + c / 2, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * w + c / 64]);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_wait_st();
-                if (keys < kTile && (keys & 15) && (!both || w == 0)) {
-                    // places past the last key up to the product's 16: whatever V holds there,
-                    // 0 times it has to be 0
-                    wait(&kv_full[v_st], int(v_ph), kTag + 12);
-                    const int n0 = 16 - (keys & 15);
-                    for (int x = row; x < n0 * C::kHalves * 8; x += 128) {
-                        const int piece = x & 7, r = (x >> 3) / C::kHalves, h = (x >> 3) % C::kHalves;
-                        *reinterpret_cast<uint4 *>(ring + v_st * C::kStageBytes + h * (kTile * 128) +
-                                                   (keys + r) * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[w]);
                 fresh = false;
                 ++done;
             }
@@ -1148,9 +1159,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                 tmem_load<32>(o_col + c, o);
                 if (row < rows) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(a.p_out + at * D + c + j) =
-                            make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    for (int j = 0; j < 32; j += 8)  // whole sectors: lanes' rows lie apart
+                        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                                         a.p_out + at * D + c + j),
+                                     "f"(o[j]), "f"(o[j + 1]), "f"(o[j + 2]), "f"(o[j + 3]), "f"(o[j + 4]),
+                                     "f"(o[j + 5]), "f"(o[j + 6]), "f"(o[j + 7])
+                                     : "memory");
                 }
             }
             tc_fence_before();
@@ -1284,7 +1298,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 struct q2_0_attn_plan {
     q2::AttnArgs args;
     int ncap, dim, n_layers;
-    bool by_rows;  // prefixes by attn_rows_kernel
+    int by_rows;  // prefixes by attn_rows_kernel with so many rows at a time, or 0
     bool bf;
     int64_t n_pages;
     void *scratch;
@@ -1313,13 +1327,17 @@ Variant variant_n(int dim, bool bf) {
 Variant variant_of(int ncap, int dim, bool bf) {
     return ncap == 32 ? variant_n<32>(dim, bf) : variant_n<64>(dim, bf);
 }
-template <int D, bool BF>
+template <int ROWS, int D, bool BF>
 Variant rows_variant() {
-    return {attn_rows_kernel<D, BF>, RowsCfg<D>::kSmem};
+    return {attn_rows_kernel<ROWS, D, BF>, RowsCfg<ROWS, D>::kSmem};
 }
-Variant rows_variant_of(int dim, bool bf) {
-    if (dim == 64) return bf ? rows_variant<64, true>() : rows_variant<64, false>();
-    return bf ? rows_variant<128, true>() : rows_variant<128, false>();
+template <int ROWS>
+Variant rows_variant_n(int dim, bool bf) {
+    if (dim == 64) return bf ? rows_variant<ROWS, 64, true>() : rows_variant<ROWS, 64, false>();
+    return bf ? rows_variant<ROWS, 128, true>() : rows_variant<ROWS, 128, false>();
+}
+Variant rows_variant_of(int rows, int dim, bool bf) {
+    return rows == 128 ? rows_variant_n<128>(dim, bf) : rows_variant_n<256>(dim, bf);
 }
 
 }  // namespace
@@ -1350,11 +1368,11 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     a.scale_log2 = d.scale * 1.44269504f;
     a.grid = sms;
     a.err = err;
-    // More than 64 rows to a prefix: 256 at a time by attn_rows_kernel.
+    // More than 64 rows to a prefix: 128 or 256 at a time by attn_rows_kernel.
     const int64_t rows = d.prefix_width ? d.n_seq * a.share : a.share;
-    p->by_rows = d.prefix_width && rows > 64;
+    p->by_rows = !d.prefix_width || rows <= 64 ? 0 : rows <= 128 ? 128 : 256;
     p->ncap = (p->by_rows ? a.share : rows) <= 32 ? 32 : 64;
-    a.spb = int(std::min<int64_t>(d.n_seq, (p->by_rows ? 256 : p->ncap) / a.share));
+    a.spb = int(std::min<int64_t>(d.n_seq, (p->by_rows ? p->by_rows : p->ncap) / a.share));
     a.row_blocks = d.prefix_width ? (a.n_seq + a.spb - 1) / a.spb : 1;
     p->dim = c.dim;
     p->n_layers = c.n_layers;
@@ -1397,7 +1415,7 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     if (ok)
         ok = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) ==
              cudaSuccess;
-    const Variant vr = rows_variant_of(p->dim, p->bf);
+    const Variant vr = rows_variant_of(p->by_rows, p->dim, p->bf);
     if (ok && p->by_rows)
         ok = cudaFuncSetAttribute(vr.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, vr.smem) ==
              cudaSuccess;
@@ -1437,7 +1455,7 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     a.own0 = 0;
     a.own1 = owners;
     if (p->by_rows) {
-        const Variant vr = rows_variant_of(p->dim, p->bf);
+        const Variant vr = rows_variant_of(p->by_rows, p->dim, p->bf);
         a.own1 = a.n_groups;
         cfg.dynamicSmemBytes = size_t(vr.smem);
         e = cudaLaunchKernelEx(&cfg, vr.fn, a);
@@ -1456,7 +1474,7 @@ int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     cfg.dynamicSmemBytes = 0;
     auto *join = p->dim == 64 ? (p->bf ? attn_join_kernel<64, true> : attn_join_kernel<64, false>)
                               : (p->bf ? attn_join_kernel<128, true> : attn_join_kernel<128, false>);
-    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->by_rows ? 128 : p->ncap, split, int(p->by_rows)));
+    return cuda_status(cudaLaunchKernelEx(&cfg, join, a, p->by_rows ? 128 : p->ncap, split, p->by_rows > 128));
 }
 
 int attn_plan_launches(const q2_0_attn_plan *p) { return p->by_rows ? 3 : 2; }
