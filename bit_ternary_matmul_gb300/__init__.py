@@ -15,6 +15,7 @@ codes q; a weight is (q - 1) * d.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -605,7 +606,9 @@ def q2_0_kv_append(cache: KvCache, layer: int, q: torch.Tensor | None, k: torch.
         qp, qs = _rows(q, "q", T, n_q, cache.dim)
         if q_out is None:
             q_out = torch.empty((T, n_q, cache.dim), dtype=cache.k.dtype, device=q.device)
-        qo = _dev(q_out, "q_out", cache.k.dtype, T * n_q * cache.dim)
+            qo = q_out.data_ptr()
+        else:
+            qo = _dev(q_out, "q_out", cache.k.dtype, T * n_q * cache.dim)
     kp, ks = _rows(k, "k", T, cache.n_kv, cache.dim)
     vp, vs = _rows(v, "v", T, cache.n_kv, cache.dim)
     if table.dim() != 2:
@@ -677,6 +680,7 @@ class AttnPlan:
             pass
 
 
+@functools.lru_cache(maxsize=256)
 def q2_0_beam_select_workspace_size(n_groups: int, n_beams: int, n_vocab: int, n_out: int) -> int:
     return int(lib().q2_0_beam_select_workspace_size(n_groups, n_beams, n_vocab, n_out))
 
@@ -710,6 +714,10 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
         token = torch.empty((G, n_out), dtype=torch.int32, device=logits.device)
         out = (torch.empty((G, n_out), dtype=torch.float32, device=logits.device),
                torch.empty_like(token), token)
+        op = [t.data_ptr() for t in out]
+    else:
+        op = [_dev(t, f"out[{i}]", torch.int32 if i else torch.float32, G * n_out)
+              for i, t in enumerate(out)]
     dp = None
     if done is not None:
         dp = _dev(done, "done", torch.bool if done.dtype == torch.bool else torch.uint8, G * W)
@@ -717,12 +725,11 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
     if wb > 0:
         if workspace is None:
             workspace = torch.empty(wb, dtype=torch.uint8, device=logits.device)
-        wp = _dev(workspace, "workspace", torch.uint8, wb)
+            wp = workspace.data_ptr()
+        else:
+            wp = _dev(workspace, "workspace", torch.uint8, wb)
     st = lib().q2_0_beam_select(logits.data_ptr(), stride, _dev(scores, "scores", torch.float32, G * W),
-                                dp, done_token, G, W, V, n_out,
-                                _dev(out[0], "out[0]", torch.float32, G * n_out),
-                                _dev(out[1], "out[1]", torch.int32, G * n_out),
-                                _dev(out[2], "out[2]", torch.int32, G * n_out), wp, wb,
+                                dp, done_token, G, W, V, n_out, op[0], op[1], op[2], wp, wb,
                                 _stream(stream))
     _check("q2_0_beam_select", st)
     return out
@@ -742,13 +749,14 @@ def q2_0_beam_reorder(cache: KvCache, parent: torch.Tensor, table: torch.Tensor,
     n, width = table.shape
     if out is None:
         out = (torch.empty_like(table), torch.empty_like(length), torch.empty_like(length))
+        op = [t.data_ptr() for t in out]
+    else:
+        op = [_dev(t, f"out[{i}]", torch.int32, n if i else n * width) for i, t in enumerate(out)]
     st = lib().q2_0_beam_reorder(cache._ref, _dev(parent, "parent", torch.int32), G, W,
                                  _dev(table, "table", torch.int32),
                                  _dev(length, "length", torch.int32, n), width,
-                                 _dev(fresh, "fresh", torch.int32, n),
-                                 _dev(out[0], "out[0]", torch.int32, n * width),
-                                 _dev(out[1], "out[1]", torch.int32, n),
-                                 _dev(out[2], "out[2]", torch.int32, n), _stream(stream))
+                                 _dev(fresh, "fresh", torch.int32, n), op[0], op[1], op[2],
+                                 _stream(stream))
     _check("q2_0_beam_reorder", st)
     return out
 
