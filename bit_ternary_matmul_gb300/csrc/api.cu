@@ -442,7 +442,8 @@ int q2_0_attn_plan_create(const q2_0_attn_desc *d, q2_0_attn_plan **plan) {
         ((reinterpret_cast<uintptr_t>(d->q) | reinterpret_cast<uintptr_t>(d->out)) & 15u) ||
         d->n_groups < 1 || d->n_seq < 1 || d->n_groups > 65535 || d->n_seq > 65535 ||
         d->n_groups * d->n_seq > 65535 || d->n_q < 1 || d->n_q > 65535 ||
-        d->n_q % d->cache.n_kv || d->n_q / d->cache.n_kv > 64 || d->width < 1 ||
+        d->n_q % d->cache.n_kv || d->n_q / d->cache.n_kv > 64 ||
+        d->n_groups * d->n_seq * d->n_q > (int64_t(1) << 28) || d->width < 1 ||
         d->prefix_width < 0 || (d->prefix_width && (!d->prefix_table || !d->prefix_len)) ||
         !(d->scale > -INFINITY && d->scale < INFINITY))
         return Q2_0_EINVAL;

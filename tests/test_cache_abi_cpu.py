@@ -65,7 +65,8 @@ def test_attention_refusals(L):
             dict(q=None), dict(out=None), dict(q=P + 4), dict(out=P + 2), dict(table=None), dict(len=None), dict(n_groups=0),
             dict(n_seq=0), dict(n_groups=300, n_seq=300), dict(n_q=0), dict(n_q=3), dict(n_q=130), dict(width=0),
             dict(prefix_width=-1), dict(prefix_table=None), dict(prefix_len=None), dict(width=1 << 27),
-            dict(prefix_width=1 << 27), dict(scale=float("inf")), dict(scale=float("nan")))]:
+            dict(prefix_width=1 << 27), dict(scale=float("inf")), dict(scale=float("nan")),
+            dict(n_groups=255, n_seq=255, n_q=8192, cache=_cache(n_kv=512, n_pages=1)))]:
         assert L.q2_0_attn_plan_create(ctypes.byref(d), ctypes.byref(h)) == q.Q2_0_EINVAL
         assert not h.value
     assert L.q2_0_attn_plan_execute(None, 0, None) == q.Q2_0_EINVAL
