@@ -36,13 +36,14 @@
 //
 // Measured on one GB300 (device time of an execute, in a graph; floors at its 6.7 TB/s
 // copy): 4 beams, 517 shared and 37 own tokens, 16 / 8 heads of 128: 11.0 us (latency:
-// deal, first tile, softmax, join). 8 beams, 50021 + 200, 32 / 8 heads of 128: 43.6 us,
-// floor 31.6; the tiles arrive at the copy rate, about 7 us pass before the first and 6
-// after the last. 4 x 16 sequences, up to 4099 + 1500, 16 heads of 64: 53.4 us, floor
-// 37.4; the products of 32 KB tiles take nearly as long as their copies. 64 sequences,
-// 131072 + up to 3000, 32 / 8 heads of 128: 192 us, floor 139; 120 of them are
-// attn_rows_kernel's, whose chain of softmax and two products per tile outlasts 64 KB
-// (tensor pipe 48 % busy, memory 53 %).
+// clocks read in an earlier version gave 2 us to the deal and 3 to 5 more to the first
+// scores). 8 beams, 50021 + 200, 32 / 8 heads of 128: 43.6 us, floor 31.6 (the same clocks:
+// first scores 6 to 8 us after the deal, with all blocks' first tiles in flight). 4 x 16
+// sequences, up to 4099 + 1500, 16 heads of 64: 53.4 us, floor 37.4 (the same clocks: about
+// 4000 to end a segment, 1200 to 1700 of work a tile). 64 sequences, 131072 + up to 3000,
+// 32 / 8 heads of 128: 192 us, floor 139. Profiled one by one with cold caches,
+// attn_rows_kernel takes 128 us of it (tensor pipe 48 % busy, memory 53 %: neither is full)
+// and attn_kernel 72 (memory 73 %).
 #include <cuda_bf16.h>
 
 #include <algorithm>
