@@ -82,7 +82,7 @@ struct Cfg {
     static constexpr int kQBufs = NCAP <= 32 ? 2 : 1;
     static constexpr int kQBytes = NCAP * D * 2;
     static constexpr int kPBytes = NCAP * kTile * 2;
-    static constexpr int kRefs = 2 * 5 * NCAP;  // floats
+    static constexpr int kRefs = 2 * 6 * NCAP;  // floats
     // references, barriers, the tile list's 12 + 2 sums
     static constexpr int kSmall = kRefs * 4 + 448;
     // K and V have stages of their own, half of the ring each. (Their consumers are different warps;
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     uint8_t *q_s = ring + C::kStages * C::kStageBytes;
     uint8_t *p_s = q_s + C::kQBufs * C::kQBytes;
-    float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 5 NCAP]
+    float *ref_s = reinterpret_cast<float *>(p_s + 2 * C::kPBytes);  // [group's 6 NCAP]
     uint64_t *bars = reinterpret_cast<uint64_t *>(ref_s + C::kRefs);
     uint8_t *v_ring = ring + C::kK * C::kStageBytes;
     uint64_t *k_full = bars, *k_empty = k_full + C::kK;
@@ -696,10 +696,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const int key = quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const float2 scale = make_float2(a.scale_log2, a.scale_log2);
-        // of the group's rows: kLift - ref, and the four warps' [4][NCAP] to be reduced
-        float *nref_s = ref_s + w * 5 * NCAP;
-        float *red_s = nref_s + NCAP;
-        float *alpha_s = red_s;  // a row's own four are read before it is written
+        // of the group's rows: kLift - ref, the factors of a raise, and the four warps' [4][NCAP] to be
+        // reduced. (The factors have floats of their own: after a raise in a segment's last tile no
+        // barrier lies between a warp that still reads them and one that writes its sums to red_s.)
+        float *nref_s = ref_s + w * 6 * NCAP;
+        float *alpha_s = nref_s + NCAP;
+        float *red_s = alpha_s + NCAP;
         const uint32_t o_col = tmem + lanes + C::kOCol + w * NCAP;
         float2 l[NCAP / 2];
         int n = 0;         // tiles so far

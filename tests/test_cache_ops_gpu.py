@@ -366,6 +366,38 @@ def test_attention_large_negative_and_zero_scale():
         c.check(f"scale {scale}")
 
 
+RAISES = [
+    # prefix lengths, own lengths, n_q, n_kv, dim, dtype: variants by the query rows of a product; 300 runs of
+    # tiles or more, so that a block's share of the tiles holds whole ones
+    ([0], [260 + i for i in range(100)], 16, 4, 128, F16),                # own tokens, 4 rows
+    ([0], [300 + 3 * i for i in range(90)], 4, 4, 64, BF16),              # own tokens, 1 row
+    ([0], [290 + i for i in range(160)], 128, 2, 128, F16),               # own tokens, 64 rows
+    ([0], [390 + i for i in range(160)], 96, 2, 64, BF16),                # own tokens, 48 rows
+    ([300 + 9 * i for i in range(40)], [0] * 400, 16, 8, 128, F16),       # prefixes of 20 rows
+    ([300 + 9 * i for i in range(40)], [3] * 480, 32, 8, 64, F16),        # prefixes of 48 rows
+    ([385] * 40, [1] * 640, 32, 8, 128, BF16),                            # prefixes of 64 rows
+]
+
+
+@pytest.mark.parametrize("plens,lens,n_q,n_kv,dim,dtype", RAISES)
+def test_attention_references_rise_to_the_last_tile(plens, lens, n_q, n_kv, dim, dtype):
+    """Every tile of 128 keys raises every reference, a segment's last one too: outputs and sums so far are
+    scaled down by the tile's factors and by nothing else."""
+    def k_of(k):  # scores rise by 12 or more (log2 units) from tile to tile
+        t = torch.arange(k.shape[1], device="cuda")[None, :, None]
+        return torch.full_like(k, dim ** -0.5) * (10.0 * (t // 128) + 1) + 0.02 * k
+    c = Attn(plens, lens, n_q, n_kv, dim, 64, dtype, seed=31, k_of=k_of)
+    c.q.copy_(torch.ones_like(c.q) + 0.02 * c.q)
+    plan = c.plan()
+    plan.execute(0)
+    _no_error()
+    c.check("rising")
+    first = c.out.clone()
+    for _ in range(20):
+        plan.execute(0)
+        assert torch.equal(c.out, first), "the same inputs gave other outputs"
+
+
 def test_attention_layers_and_streams():
     c = Attn([300], [40, 50], 8, 4, 64, 32, F16, seed=6, layers=3, layer=2)
     plan = c.plan()
