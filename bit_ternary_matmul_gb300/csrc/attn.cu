@@ -67,6 +67,7 @@ constexpr bool regs_fit(int few, int many) { return 128 * few + 256 * many == 38
 constexpr int kTag = 300;      // waits' tags: 301..
 constexpr float kLift = 7.0f;  // p = 2^(s - ref + kLift)
 constexpr float kSlack = 8.0f; // how far a score may pass the reference
+constexpr float kFused = 1.6e7f; // references up to which a score is scaled and reduced by it in one operation
 // Cost of a tile, and of a segment beside its tiles, for the shares. Measured (four groups of
 // sixteen, 4099 shared and up to 1500 own tokens, dim 64): 4 of an item 60.5 us, 8 55.9, 14 53.4,
 // 20 54.3, 28 58.8; at dim 128 it hardly matters.
@@ -134,7 +135,7 @@ struct AttnArgs {
     // scratch
     int2 *p_item, *s_item; // items' records: the first one, how many (of items with keys)
     float *p_out, *s_out;  // records' outputs: prefix [rec][NCAP or 128][dim], own [rec][share][dim]
-    float2 *p_ml, *s_ml;   // their (reference, sum), a row each; sum 0: nothing
+    float2 *p_ml, *s_ml;   // their (reference - kLift, sum), a row each; sum 0: nothing
     int grid;
     unsigned long long *err;
 };
@@ -696,6 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const int key = quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const float2 scale = make_float2(a.scale_log2, a.scale_log2);
+        // A reference is a rounded product of a score and the scale. A score scaled and reduced by it in one
+        // fused operation is off it by that rounding, half a unit at most up to kFused; beyond (finite, if
+        // absurd, scores) the largest weights could overflow or vanish, so that every tile goes the way
+        // of a raise, where the products are rounded by themselves as the reference is.
+        bool far = false;
         // of the group's rows: kLift - ref, the factors of a raise, and the four warps' [4][NCAP] to be
         // reduced. (The factors have floats of their own: after a raise in a segment's last tile no
         // barrier lies between a warp that still reads them and one that writes its sums to red_s.)
@@ -752,14 +758,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const bool in = key < keys;
                     const uint32_t sa = tmem + lanes + w * NCAP;
                     float v[W];
-                    auto exponents = [&]() {
+                    auto exponents = [&](auto fused) {
+                        auto scaled = [&](float2 x, float2 r) {
+                            return fused ? fma2(x, scale, r) : add2(fma2(x, scale, make_float2(0.0f, 0.0f)), r);
+                        };
 #pragma unroll
                         for (int j = 0; j < W; j += 4) {
                             const float4 r = *reinterpret_cast<const float4 *>(nref_s + j);
                             *reinterpret_cast<float2 *>(v + j) =
-                                fma2(make_float2(v[j], v[j + 1]), scale, make_float2(r.x, r.y));
+                                scaled(make_float2(v[j], v[j + 1]), make_float2(r.x, r.y));
                             *reinterpret_cast<float2 *>(v + j + 2) =
-                                fma2(make_float2(v[j + 2], v[j + 3]), scale, make_float2(r.z, r.w));
+                                scaled(make_float2(v[j + 2], v[j + 3]), make_float2(r.z, r.w));
                         }
                         if (keys < kTile) {
 #pragma unroll
@@ -769,11 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tmem_load<W>(sa, v);
                     bool raise = fresh;
                     if (!raise) {
-                        exponents();
+                        exponents(std::true_type{});
                         float most = v[0];
 #pragma unroll
                         for (int j = 1; j < W - 1; j += 2) most = max3(most, v[j], v[j + 1]);
-                        raise = group_any(w, fmaxf(most, v[W - 1]) > kSlack + kLift);
+                        raise = group_any(w, far || fmaxf(most, v[W - 1]) > kSlack + kLift);
                         if (raise) tmem_load<W>(sa, v);
                     }
                     if (raise) {
@@ -782,16 +791,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         for (int j = 0; j < W; ++j) v[j] = in ? v[j] * scale.x : -INFINITY;
                         across_to<W, true>(v, red_s + quarter * NCAP);
                         group_sync(w);
+                        bool beyond = false;
                         if (key < W) {
-                            const float old = fresh ? -INFINITY : kLift - nref_s[key];
-                            float m = fmaxf(fmaxf(red_s[key], red_s[NCAP + key]),
-                                            fmaxf(red_s[2 * NCAP + key], red_s[3 * NCAP + key]));
+                            const float m = fmaxf(fmaxf(red_s[key], red_s[NCAP + key]),
+                                                  fmaxf(red_s[2 * NCAP + key], red_s[3 * NCAP + key]));
+                            const float old = fresh ? INFINITY : nref_s[key];
                             // no key counts (scores of -inf): any finite reference does
-                            m = fmaxf(fmaxf(m, old), -1e30f);
-                            alpha_s[key] = ex2(old - m);
-                            nref_s[key] = kLift - m;
+                            const float now = fminf(kLift - fmaxf(m, -1e30f), old);
+                            alpha_s[key] = ex2(now - old);
+                            nref_s[key] = now;
+                            beyond = fabsf(now) > kFused;
                         }
-                        group_sync(w);
+                        far = group_any(w, beyond);
                         if (fresh) {
 #pragma unroll
                             for (int j = 0; j < NCAP / 2; ++j) l[j] = make_float2(0.0f, 0.0f);
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             tmem_store<W>(o_col, v);
                         }
                         tmem_load<W>(sa, v);
-                        exponents();
+                        exponents(std::false_type{});
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -870,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 across_to<W, false>(v, red_s + quarter * NCAP);
                 group_sync(w);
                 if (key < rows)
-                    ml[key] = make_float2(kLift - nref_s[key],
+                    ml[key] = make_float2(-nref_s[key],
                                           (red_s[key] + red_s[NCAP + key]) +
                                               (red_s[2 * NCAP + key] + red_s[3 * NCAP + key]));
                 group_sync(w);  // nref_s and red_s are free again
@@ -1107,11 +1118,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                 most[0] = fmaxf(max3(most[0], most[1], most[2]), most[3]);
                 const bool raise = fresh || most[0] + nref > kSlack + kLift;
                 if (__any_sync(0xffffffffu, raise)) {
-                    const float old = fresh ? -INFINITY : kLift - nref;
                     // no key counts (scores of -inf): any finite reference does
-                    const float ref = raise ? fmaxf(fmaxf(most[0], old), -1e30f) : old;
-                    const float f = fresh ? 0.0f : ex2(old - ref);
-                    nref = kLift - ref;
+                    const float now = kLift - fmaxf(most[0], -1e30f);
+                    const float next = fresh ? now : raise ? fminf(now, nref) : nref;
+                    const float f = fresh ? 0.0f : ex2(next - nref);
+                    nref = next;
                     l *= f;
                     if (!fresh) {  // the products into this output so far are done
                         wait(&o_done[w], done - 1, kTag + 14);
@@ -1164,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
             // ---- the segment's output, reference and sum
             const int rows = both ? s.rows - 128 * w : s.rows;  // of the group
             const int64_t at = (record_of(a, s) + w) * 128 + row;
-            if (row < rows) a.p_ml[at] = fresh ? make_float2(-1e30f, 0.0f) : make_float2(kLift - nref, l);
+            if (row < rows) a.p_ml[at] = fresh ? make_float2(-1e30f, 0.0f) : make_float2(-nref, l);
             if (fresh) continue;
             wait(&o_done[w], done - 1, kTag + 13);
             tc_fence_after();

@@ -398,6 +398,51 @@ def test_attention_references_rise_to_the_last_tile(plens, lens, n_q, n_kv, dim,
         assert torch.equal(c.out, first), "the same inputs gave other outputs"
 
 
+HUGE = [
+    ([0], [1, 129, 300, 700], 8, 2, 128, F16), ([400], [1, 129, 0, 200], 8, 2, 64, BF16),
+    ([0], [300, 500], 64, 1, 64, F16), ([400], [5] * 12, 8, 2, 128, BF16), ([400], [140, 0, 5] * 10, 8, 2, 128, F16),
+    ([400], [140, 0] * 40, 8, 2, 64, BF16)]
+
+
+@pytest.mark.parametrize("size", [26, 29, 33])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("plens,lens,n_q,n_kv,dim,dtype", HUGE)
+def test_attention_huge_finite_scores(plens, lens, n_q, n_kv, dim, dtype, sign, size):
+    """Scores of about +-2^size (log2 units) in which one key is ahead by far: the output is its value. The
+    weight and the output are rounded to the cache's type once each: 2 u |v|."""
+    _one_key_ahead(plens, lens, n_q, n_kv, dim, dtype, sign, size)
+
+
+def _one_key_ahead(plens, lens, n_q, n_kv, dim, dtype, sign, size):
+    c_k = 1.37 * 2.0 ** ((size + 2.97 - math.log2(dim)) / 2)   # of elements: dim c_k^2 / sqrt(dim) is the score's size
+    groups, calls, win = len(plens), [], []
+
+    def k_of(k):
+        g = torch.Generator(device="cuda").manual_seed(len(calls))
+        n = k.shape[1]
+        m = 0.3 + 0.3 * torch.rand((k.shape[0], n, 1), generator=g, device="cuda")
+        best = 0.8 if len(calls) < groups else 0.9     # a sequence's own winner is ahead of its prefix's
+        if sign < 0:
+            m, best = 1.3 - m, 1 - best
+        calls.append(n)
+        win.append((7 * len(calls) + n // 2) % max(1, n))
+        if n:
+            m[:, win[-1]] = best
+        return m.expand_as(k) * (sign * c_k)
+    c = Attn(plens, lens, n_q, n_kv, dim, 16, dtype, seed=17, k_of=k_of)
+    c.q.fill_(c_k)
+    plan = c.plan()
+    plan.execute(0)
+    _no_error()
+    share = n_q // n_kv
+    for b, n in enumerate(lens):
+        i = groups + b if n else b // (len(lens) // groups)
+        if calls[i]:
+            e = c.vs[i][:, win[i]].double().repeat_interleave(share, 0)
+            tol = 2 * U[dtype] * (1 + 2.0 ** -8) * e.abs() + 2.0 ** -25
+            assert ((c.out[b].double() - e).abs() <= tol).all(), (b, n)
+
+
 def test_attention_layers_and_streams():
     c = Attn([300], [40, 50], 8, 4, 64, 32, F16, seed=6, layers=3, layer=2)
     plan = c.plan()
