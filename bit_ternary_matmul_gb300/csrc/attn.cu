@@ -45,6 +45,7 @@
 // attn_rows_kernel takes 128 us of it (tensor pipe 48 % busy, memory 53 %: neither is full)
 // and attn_kernel 72 (memory 73 %).
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include <algorithm>
 #include <new>
@@ -797,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                                   fmaxf(red_s[2 * NCAP + key], red_s[3 * NCAP + key]));
                             const float old = fresh ? INFINITY : nref_s[key];
                             // no key counts (scores of -inf): any finite reference does
-                            const float now = fminf(kLift - fmaxf(m, -1e30f), old);
+                            const float now = fminf(kLift - fmaxf(m, -FLT_MAX), old);
                             alpha_s[key] = ex2(now - old);
                             nref_s[key] = now;
                             beyond = fabsf(now) > kFused;
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             float2 *ml = (pre ? a.p_ml : a.s_ml) + at;
             const int rows = s.rows;
             if (fresh) {  // the other group had the only tile
-                if (key < rows) ml[key] = make_float2(-1e30f, 0.0f);
+                if (key < rows) ml[key] = make_float2(-FLT_MAX, 0.0f);
                 continue;
             }
             with_columns<NCAP>(s.N, [&](auto columns) {
@@ -1119,7 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                 const bool raise = fresh || most[0] + nref > kSlack + kLift;
                 if (__any_sync(0xffffffffu, raise)) {
                     // no key counts (scores of -inf): any finite reference does
-                    const float now = kLift - fmaxf(most[0], -1e30f);
+                    const float now = kLift - fmaxf(most[0], -FLT_MAX);
                     const float next = fresh ? now : raise ? fminf(now, nref) : nref;
                     const float f = fresh ? 0.0f : ex2(next - nref);
                     nref = next;
@@ -1175,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
             // ---- the segment's output, reference and sum
             const int rows = both ? s.rows - 128 * w : s.rows;  // of the group
             const int64_t at = (record_of(a, s) + w) * 128 + row;
-            if (row < rows) a.p_ml[at] = fresh ? make_float2(-1e30f, 0.0f) : make_float2(-nref, l);
+            if (row < rows) a.p_ml[at] = fresh ? make_float2(-FLT_MAX, 0.0f) : make_float2(-nref, l);
             if (fresh) continue;
             wait(&o_done[w], done - 1, kTag + 13);
             tc_fence_after();

@@ -443,6 +443,12 @@ def _one_key_ahead(plens, lens, n_q, n_kv, dim, dtype, sign, size):
             assert ((c.out[b].double() - e).abs() <= tol).all(), (b, n)
 
 
+@pytest.mark.parametrize("plens,lens,n_q,n_kv,dim,dtype", [h for h in HUGE if h[-1] is BF16])
+def test_attention_scores_near_the_largest_float(plens, lens, n_q, n_kv, dim, dtype):
+    for sign in (1, -1):
+        _one_key_ahead(plens, lens, n_q, n_kv, dim, dtype, sign, 119)
+
+
 def test_attention_layers_and_streams():
     c = Attn([300], [40, 50], 8, 4, 64, 32, F16, seed=6, layers=3, layer=2)
     plan = c.plan()
