@@ -2,8 +2,10 @@
 
 Thin ctypes marshalling over the C ABI declared in ``include/q2_0.h``: the
 functions here carry the same names as the C entry points, check tensor
-dtype/device/contiguity, pass ``data_ptr()`` values and the current CUDA stream,
-and raise on a non-OK status. Every result is computed by the library's CUDA
+dtype/device/contiguity, pass ``data_ptr()`` values and the current CUDA stream
+(or ``stream``: outputs and workspaces that a call makes are then that stream's
+memory, and a user on another one waits for it and calls record_stream), and
+raise on a non-OK status. Every result is computed by the library's CUDA
 kernels; there is no CPU path. PyTorch provides device memory and streams only.
 
 Q2_0 (sources: "WebGPU: add Q2_0 support", bisque.today write-up of llama.cpp
@@ -223,6 +225,22 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A buffer that a call allocates for itself: memory of the stream it runs on, as a tensor made
+    under torch.cuda.stream(...) has. (The current stream's may be in use there until later, and is
+    handed out again there as soon as the last reference goes, whatever runs on `stream`.)"""
+    if stream is not None and device.type == "cuda":
+        handle = _stream(stream)
+        if handle != _stream(None):
+            if not isinstance(stream, torch.cuda.Stream):
+                # (0 and 1 are the legacy default stream's handles)
+                stream = (torch.cuda.ExternalStream(handle, device) if handle > 1
+                          else torch.cuda.default_stream(device))
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: torch.Tensor, name: str, dtype, numel: int = 0):
     try:
         if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
@@ -259,7 +277,7 @@ def q2_0_mul_mat_vec(w: torch.Tensor, x: torch.Tensor, N: int, K: int, ncols: in
     """y[c][n] = sum_k W[n][k] x[c][k]; w uint8 packed, x f32 [ncols][K]."""
     ncols = x.shape[0] if (ncols is None and x.dim() == 2) else (ncols or 1)
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     st = lib().q2_0_mul_mat_vec(_dev(w, "w", torch.uint8, packed_bytes(N, K)),
                                 _dev(x, "x", torch.float32, ncols * K),
                                 _dev(y, "y", torch.float32, ncols * N), N, K, ncols, _stream(stream))
@@ -273,7 +291,7 @@ def q2_0_mul_mat_vec_f16(w: torch.Tensor, x: torch.Tensor, N: int, K: int,
     """As q2_0_mul_mat_vec with x F16 [ncols][K]."""
     ncols = x.shape[0] if (ncols is None and x.dim() == 2) else (ncols or 1)
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     st = lib().q2_0_mul_mat_vec_f16(_dev(w, "w", torch.uint8, packed_bytes(N, K)),
                                     _dev(x, "x", torch.float16, ncols * K),
                                     _dev(y, "y", torch.float32, ncols * N), N, K, ncols,
@@ -288,7 +306,7 @@ def q2_0_mul_mat_vec_workspace_size(K: int, ncols: int) -> int:
 
 def q2_0_mul_mat_vec_ws(w, x, N, K, ncols, workspace: torch.Tensor, y=None, stream=None):
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     need = q2_0_mul_mat_vec_workspace_size(K, ncols)
     st = lib().q2_0_mul_mat_vec_ws(_dev(w, "w", torch.uint8, packed_bytes(N, K)),
                                    _dev(x, "x", torch.float32, ncols * K),
@@ -310,7 +328,7 @@ def q2_0_mul_mat_vec_noalloc(w: torch.Tensor, x: torch.Tensor, N: int, K: int,
     """
     ncols = x.shape[0] if (ncols is None and x.dim() == 2) else (ncols or 1)
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     st = lib().q2_0_mul_mat_vec_noalloc(_dev(w, "w", torch.uint8, packed_bytes(N, K)),
                                         _dev(x, "x", torch.float32, ncols * K),
                                         _dev(y, "y", torch.float32, ncols * N), N, K, ncols,
@@ -368,7 +386,7 @@ def q2_0_mul_mat(w: torch.Tensor, x: torch.Tensor, N: int, K: int, M: int | None
     """Y[m][n] = sum_k W[n][k] X[m][k]; x f32 [M][K] -> y f32 [M][N]."""
     M = x.shape[0] if M is None else M
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_bytes = workspace.numel()
@@ -428,7 +446,7 @@ def q2_0_mul_mat_f16(w: torch.Tensor, x: torch.Tensor, N: int, K: int, M: int | 
     Q2_0_PREC_F16)."""
     M = x.shape[0] if M is None else M
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_bytes = workspace.numel()
@@ -447,7 +465,7 @@ def q2_0_get_rows(table: torch.Tensor, n_rows: int, K: int, ids: torch.Tensor,
     """out[r] = row ids[r] of the Q2_0 table as F32 (bit-exact)."""
     n_ids = ids.numel()
     if out is None:
-        out = torch.empty((n_ids, K), dtype=torch.float32, device=ids.device)
+        out = _empty((n_ids, K), torch.float32, ids.device, stream)
     if n_ids == 0:
         return out
     st = lib().q2_0_get_rows(_dev(table, "table", torch.uint8, packed_bytes(n_rows, K)), n_rows, K,
@@ -473,12 +491,12 @@ def q2_0_mul_mat_id(w: torch.Tensor, n_expert: int, N: int, K: int, x: torch.Ten
     n_tokens, n_used = ids.shape
     n_x = 1 if x.dim() == 2 else x.shape[1]
     if y is None:
-        y = torch.empty((n_tokens, n_used, N), dtype=torch.float32, device=ids.device)
+        y = _empty((n_tokens, n_used, N), torch.float32, ids.device, stream)
     if n_tokens == 0:
         return y
     need = q2_0_mul_mat_id_workspace_size(K, n_tokens, n_x)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+        workspace = _empty(need, torch.uint8, ids.device, stream)
     wsp = _dev(workspace, "workspace", torch.uint8, need) if need > 0 else None
     st = lib().q2_0_mul_mat_id(_dev(w, "w", torch.uint8, n_expert * packed_bytes(N, K)), n_expert,
                                N, K, _dev(x, "x", torch.float32, n_tokens * n_x * K), n_x,
@@ -498,7 +516,7 @@ def q2_0_split_layout(w: torch.Tensor, N: int, K: int, dst: torch.Tensor | None 
     """18-byte blocks -> split layout (codes, then 256-byte aligned fp16 scales)."""
     nbytes = q2_0_split_bytes(N, K)
     if dst is None:
-        dst = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+        dst = _empty(nbytes, torch.uint8, w.device, stream)
     st = lib().q2_0_split_layout(_dev(w, "w", torch.uint8, packed_bytes(N, K)),
                                  _dev(dst, "dst", torch.uint8, nbytes), N, K, _stream(stream))
     _check("q2_0_split_layout", st)
@@ -509,7 +527,7 @@ def q2_0_join_layout(src: torch.Tensor, N: int, K: int, w: torch.Tensor | None =
                      stream=None) -> torch.Tensor:
     """Split layout -> 18-byte blocks."""
     if w is None:
-        w = torch.empty(packed_bytes(N, K), dtype=torch.uint8, device=src.device)
+        w = _empty(packed_bytes(N, K), torch.uint8, src.device, stream)
     st = lib().q2_0_join_layout(_dev(src, "src", torch.uint8, q2_0_split_bytes(N, K)),
                                 _dev(w, "w", torch.uint8, packed_bytes(N, K)), N, K, _stream(stream))
     _check("q2_0_join_layout", st)
@@ -520,7 +538,7 @@ def q2_0_mul_mat_vec_split(w: torch.Tensor, x: torch.Tensor, N: int, K: int, nco
                            y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[c][n] = sum_k W[n][k] x[c][k] with W in the split layout."""
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     st = lib().q2_0_mul_mat_vec_split(_dev(w, "w", torch.uint8, q2_0_split_bytes(N, K)),
                                       _dev(x, "x", torch.float32, ncols * K),
                                       _dev(y, "y", torch.float32, ncols * N), N, K, ncols,
@@ -533,7 +551,7 @@ def q2_0_quantize_ref(src: torch.Tensor, nrows: int, K: int, dst: torch.Tensor |
                       stream=None) -> torch.Tensor:
     """Reference quantizer: f32 [nrows][K] -> packed uint8 blocks."""
     if dst is None:
-        dst = torch.empty(packed_bytes(nrows, K), dtype=torch.uint8, device=src.device)
+        dst = _empty(packed_bytes(nrows, K), torch.uint8, src.device, stream)
     st = lib().q2_0_quantize_ref(_dev(src, "src", torch.float32, nrows * K),
                                  _dev(dst, "dst", torch.uint8, packed_bytes(nrows, K)), nrows, K,
                                  _stream(stream))
@@ -605,7 +623,7 @@ def q2_0_kv_append(cache: KvCache, layer: int, q: torch.Tensor | None, k: torch.
         n_q = q.shape[1] if q.dim() == 3 else q.shape[1] // cache.dim
         qp, qs = _rows(q, "q", T, n_q, cache.dim)
         if q_out is None:
-            q_out = torch.empty((T, n_q, cache.dim), dtype=cache.k.dtype, device=q.device)
+            q_out = _empty((T, n_q, cache.dim), cache.k.dtype, q.device, stream)
             qo = q_out.data_ptr()
         else:
             qo = _dev(q_out, "q_out", cache.k.dtype, T * n_q * cache.dim)
@@ -711,9 +729,9 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
         raise ValueError("logits must have contiguous rows, evenly apart")
     n_out = W if n_out is None else n_out
     if out is None:
-        token = torch.empty((G, n_out), dtype=torch.int32, device=logits.device)
-        out = (torch.empty((G, n_out), dtype=torch.float32, device=logits.device),
-               torch.empty_like(token), token)
+        token = _empty((G, n_out), torch.int32, logits.device, stream)
+        out = (_empty((G, n_out), torch.float32, logits.device, stream),
+               _empty((G, n_out), torch.int32, logits.device, stream), token)
         op = [t.data_ptr() for t in out]
     else:
         op = [_dev(t, f"out[{i}]", torch.int32 if i else torch.float32, G * n_out)
@@ -724,7 +742,7 @@ def q2_0_beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int | No
     wp, wb = None, q2_0_beam_select_workspace_size(G, W, V, n_out)
     if wb > 0:
         if workspace is None:
-            workspace = torch.empty(wb, dtype=torch.uint8, device=logits.device)
+            workspace = _empty(wb, torch.uint8, logits.device, stream)
             wp = workspace.data_ptr()
         else:
             wp = _dev(workspace, "workspace", torch.uint8, wb)
@@ -748,7 +766,7 @@ def q2_0_beam_reorder(cache: KvCache, parent: torch.Tensor, table: torch.Tensor,
     G, W = parent.shape
     n, width = table.shape
     if out is None:
-        out = (torch.empty_like(table), torch.empty_like(length), torch.empty_like(length))
+        out = tuple(_empty(t.shape, t.dtype, t.device, stream) for t in (table, length, length))
         op = [t.data_ptr() for t in out]
     else:
         op = [_dev(t, f"out[{i}]", torch.int32, n if i else n * width) for i, t in enumerate(out)]
@@ -785,7 +803,7 @@ def q2_0_g128_to_g64(src: torch.Tensor, nrows: int, K: int, dst: torch.Tensor | 
                     stream=None) -> torch.Tensor:
     """Exact repack of a group-128 matrix into the 64-weight layout (uint8)."""
     if dst is None:
-        dst = torch.empty(packed_bytes(nrows, K), dtype=torch.uint8, device=src.device)
+        dst = _empty(packed_bytes(nrows, K), torch.uint8, src.device, stream)
     st = lib().q2_0_g128_to_g64(_dev(src, "src", torch.uint8, packed_bytes_g128(nrows, K)),
                                _dev(dst, "dst", torch.uint8, packed_bytes(nrows, K)), nrows, K,
                                _stream(stream))
@@ -797,7 +815,7 @@ def q2_0_g128_get_rows(table: torch.Tensor, n_rows: int, K: int, ids: torch.Tens
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     n_ids = ids.numel()
     if out is None:
-        out = torch.empty((n_ids, K), dtype=torch.float32, device=ids.device)
+        out = _empty((n_ids, K), torch.float32, ids.device, stream)
     if n_ids == 0:
         return out
     st = lib().q2_0_g128_get_rows(_dev(table, "table", torch.uint8, packed_bytes_g128(n_rows, K)),
@@ -812,7 +830,7 @@ def q2_0_g128_mul_mat_vec(w: torch.Tensor, x: torch.Tensor, N: int, K: int,
                          stream=None) -> torch.Tensor:
     ncols = x.shape[0] if (ncols is None and x.dim() == 2) else (ncols or 1)
     if y is None:
-        y = torch.empty((ncols, N), dtype=torch.float32, device=x.device)
+        y = _empty((ncols, N), torch.float32, x.device, stream)
     st = lib().q2_0_g128_mul_mat_vec(_dev(w, "w", torch.uint8, packed_bytes_g128(N, K)),
                                     _dev(x, "x", torch.float32, ncols * K),
                                     _dev(y, "y", torch.float32, ncols * N), N, K, ncols,
