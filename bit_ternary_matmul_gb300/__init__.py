@@ -780,8 +780,9 @@ def q2_0_beam_reorder(cache: KvCache, parent: torch.Tensor, table: torch.Tensor,
 
 
 def q2_0_test_inject_stall(stage: int, wait_limit_ns: int) -> None:
-    """Test only: the next fp4 mat-vec launch on the current device stalls before
-    pipeline stage `stage` and its waits give up after wait_limit_ns."""
+    """Test only: the next fp4 mat-vec launch on the current device stalls before pipeline stage
+    `stage` and its waits give up after wait_limit_ns; or the next attention execute, if it comes
+    first, about `stage` tiles into each block's share (after its usual second)."""
     _check("q2_0_test_inject_stall", lib().q2_0_test_inject_stall(int(stage), int(wait_limit_ns)))
 
 

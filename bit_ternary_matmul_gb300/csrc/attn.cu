@@ -139,6 +139,7 @@ struct AttnArgs {
     float2 *p_ml, *s_ml;   // their (reference - kLift, sum), a row each; sum 0: nothing
     int grid;
     unsigned long long *err;
+    int stall;  // test hook (q2_0_test_inject_stall): > 0: copies of K end stall - 1 tiles' units into a block's share
 };
 
 // An owner of tiles: a group's prefix (o < n_groups) or a sequence.
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFew));
     if (warp == 0 || warp == 2) {
         // ------------------------- K (warp 0) and V (warp 2) copies -------------------------
+        if (warp == 0 && a.stall) walk.end = min(walk.end, walk.at + (a.stall - 1) * kTileCost);
         copy_tiles<D>(a, walk, warp ? &a.v_map : &a.k_map, warp ? C::kV : C::kK, warp ? v_ring : ring,
                       warp ? v_full : k_full, warp ? v_empty : k_empty);
     } else if (warp == 1) {
@@ -968,6 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
 
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsFew));
     if (warp == 0 || warp == 2) {
+        if (warp == 0 && a.stall) walk.end = min(walk.end, walk.at + (a.stall - 1) * kTileCost);
         copy_tiles<D>(a, walk, warp ? &a.v_map : &a.k_map, warp ? C::kV : C::kK, warp ? v_ring : ring,
                       warp ? v_full : k_full, warp ? v_empty : k_empty);
     } else if (warp == 1) {
@@ -1395,6 +1398,7 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     a.scale_log2 = d.scale * 1.44269504f;
     a.grid = sms;
     a.err = err;
+    a.stall = 0;
     // More than 64 rows to a prefix: 128 or 256 at a time by attn_rows_kernel.
     const int64_t rows = d.prefix_width ? d.n_seq * a.share : a.share;
     p->by_rows = !d.prefix_width || rows <= 64 ? 0 : rows <= 128 ? 128 : 256;
@@ -1438,6 +1442,9 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     const size_t o_pml = take(p_rows * 8), o_sml = take(s_rows * 8);
     p->scratch = nullptr;
     if (ok) ok = cudaMalloc(&p->scratch, at) == cudaSuccess;
+    // An execute whose waits ran out may leave items without their records' places: the join then
+    // finds none or an earlier execute's, never what lay in this memory before.
+    if (ok) ok = cudaMemset(p->scratch, 0, o_p) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess;
     const Variant v = variant_of(p->ncap, p->dim, p->bf);
     if (ok)
         ok = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) ==
@@ -1465,6 +1472,7 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
 int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     AttnArgs a = p->args;
     a.row0 = int(layer * p->n_pages);
+    a.stall = take_stall(nullptr);
     const Variant v = variant_of(p->ncap, p->dim, p->bf);
     // Each launch may be set up while the one before it drains; both wait for its
     // results (griddepcontrol.wait) before they read anything.
