@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         int st = 0, seg = 0;
         uint32_t ph = 0;
         int n = 0;  // tiles so far
+        int loads = 0;  // of Q so far
         bool ok = true;
         // the segment's Q, into buffer seg % kQBufs
         auto load_q = [&](const Segment &q, int i) {
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     tma_load_3d(q_s + qb * C::kQBytes + h * (NCAP * 128), pre ? &a.qp_map : &a.qs_map,
                                 h * 64, q.head * a.share, seq, &q_full[qb]);
             }
+            ++loads;
             __syncwarp();
             return true;
         };
@@ -645,6 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             if (C::kQBufs == 1 && ok && more) ok = load_q(ahead, seg + 1);
         }
+        if (!ok)  // let the copies in flight land (bounded)
+            for (int i = max(0, loads - C::kQBufs); i < loads; ++i)
+                mbar_wait(&q_full[i % C::kQBufs], uint32_t(i / C::kQBufs) & 1u, a.err, kTag + 2);
     } else if (warp == 3) {
         // ------------------------------- the second products -------------------------------
         const bool leader = elect_one();
@@ -979,6 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
         int st = 0, seg = 0;
         uint32_t ph = 0;
         int count[2] = {0, 0};  // the groups' tiles so far
+        int loads = 0;          // of Q so far
         bool ok = true;
         const uint32_t idesc = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(kTile >> 3) << 17) |
                                (uint32_t(128 >> 4) << 24);
@@ -993,6 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                     tma_load_3d(q_s + h * (C::kRows * 128), &a.qp_map, h * 64, s.head * a.share,
                                 s.owner * a.n_seq + s.block * a.spb, q_full);
             }
+            ++loads;
             __syncwarp();
             ok = __all_sync(0xffffffffu, mbar_wait_spin(q_full, uint32_t(seg) & 1u, a.err, kTag + 6));
             const bool both = ROWS > 128 && s.rows > 128;
@@ -1023,6 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const __grid_con
                 next_stage<C::kK>(st, ph);
             }
         }
+        if (!ok && loads > 0)  // let the copies in flight land (bounded)
+            mbar_wait(q_full, uint32_t(loads - 1) & 1u, a.err, kTag + 2);
     } else if (warp == 3) {
         // ------------------------------- the second products -------------------------------
         const bool leader = elect_one();

@@ -62,3 +62,12 @@ def test_stalled_attention_times_out_and_recovers(plens, lens, n_q, n_kv, dim, d
         assert q.q2_0_get_error() == (0, 0)
         c.check("after the second stall")
     plan.close()
+
+
+@pytest.mark.parametrize("plens,lens,n_q,n_kv,dim,dtype", [
+    ([0], [100 + i % 150 for i in range(400)], 8, 2, 128, F16),         # 5 or more segments a block: the next one's
+    ([0], [100 + i % 150 for i in range(200)], 96, 2, 64, BF16),        # queries are copied ahead, or behind the last
+    ([300] * 90, [5] * 90 * 32, 16, 4, 64, F16)])                       # prefixes of 128 rows
+def test_stalled_attention_with_queries_in_flight(plens, lens, n_q, n_kv, dim, dtype):
+    test_stalled_attention_times_out_and_recovers(plens, lens, n_q, n_kv, dim, dtype, 0)
+    test_stalled_attention_times_out_and_recovers(plens, lens, n_q, n_kv, dim, dtype, 8)
