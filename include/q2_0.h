@@ -456,9 +456,11 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_
  *   the device, and one captured execute serves all its steps.
  * Precision: scores, softmax sums and output sums are f32; each weight
  * exp(score - reference) enters its product with v rounded to the cache's type
- * (2^-11 or 2^-8 of itself), and so is the output: it
- * is within u (sum p|v| + |out|) and f32 rounding of the exact one, u that
- * rounding and p the softmax weights.
+ * (2^-11 or 2^-8 of itself; an F16 weight below 2^-21 of its row's largest by
+ * 2^-32 of that at most, F16 having a fixed spacing there), and so is the output: it is
+ * within u (sum p|v| + |out|), F16: + 2^-32 sum |v|, and f32 rounding of the exact
+ * one, u that rounding, p the softmax weights and the sums over the row's keys. Scores
+ * have to be finite in f32; BF16 values of v above 2^90 may overflow on the way.
  * A length outside [0, width * page] is taken as the nearer bound, and a page
  * id outside [0, n_pages) as page 0; both record Q2_0_DEVERR_BAD_ID with info =
  * the sequence (or n_groups * n_seq + the group).

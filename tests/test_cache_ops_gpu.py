@@ -449,6 +449,42 @@ def test_attention_scores_near_the_largest_float(plens, lens, n_q, n_kv, dim, dt
         _one_key_ahead(plens, lens, n_q, n_kv, dim, dtype, sign, 119)
 
 
+@pytest.mark.parametrize("plens,lens,n_q,n_kv", [([0], [128] * 3, 8, 2), ([0], [128] * 2, 64, 1), ([128], [0] * 40, 8, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_small_weights_behind_a_sink(plens, lens, n_q, n_kv, dtype):
+    """One key takes nearly all the weight and has no value; the others lie 2^-24.349 below it. F16 weights this
+    small have a fixed spacing: in it theirs is 100.49, so that rounding moves them all by 0.49 of it. The bound is
+    the declared one: u (sum p|v| + |out|), F16: 2^-32 sum |v| more, and f32 rounding."""
+    c = Attn(plens, lens, n_q, n_kv, 64, 64, dtype, seed=23, scale=24.349 * math.log(2), k_of=lambda k: k * 0)
+    c.q.zero_()
+    c.q[..., 0] = 1
+    c.v.mul_(1000)
+    rows = [(c.ptable[0], plens[0], 0)] + [(c.table[b], n, 1 + b) for b, n in enumerate(lens)]
+    for row, n, i in rows:
+        if n:
+            c.vs[i] = c.vs[i] * 1000
+            c.vs[i][:, 0] = 0
+            c.ks[i][:, 0, 0] = 1
+            c.k[0, int(row[0]), :, 0, 0] = 1
+            c.v[0, int(row[0]), :, 0] = 0
+    plan = c.plan()
+    plan.execute(0)
+    _no_error()
+    u, worst = U[dtype], 0.0
+    for b, n in enumerate(lens):
+        i = 1 + b if n else 0
+        s = c.ks[i][:, :, 0].double() * c.scale
+        p, v = torch.softmax(s, -1), c.vs[i].double()
+        e, a = (torch.einsum("ht,htd->hd", p, x).repeat_interleave(n_q // n_kv, 0) for x in (v, v.abs()))
+        err = (c.out[b].double() - e).abs()
+        # f32: the scores' one product and its scaling (2^-23 of 24.4, as in the head of this file), 64 additions
+        plain = u * (1 + 2.0 ** -8) * (a + e.abs()) + 2.0 ** -23 * (2 * 3 * 17 + 64) * a + 2.0 ** -25
+        more = 2.0 ** -32 * v.abs().sum(1).repeat_interleave(n_q // n_kv, 0) if dtype is F16 else 0.0
+        assert (err <= plain + more).all()
+        worst = max(worst, float((err / plain).max()))
+    assert dtype is BF16 or worst > 1, "the small weights' own term is not needed"
+
+
 def test_attention_layers_and_streams():
     c = Attn([300], [40, 50], 8, 4, 64, 32, F16, seed=6, layers=3, layer=2)
     plan = c.plan()
