@@ -169,7 +169,8 @@ __device__ __forceinline__ long long share_begin(long long c, long long T, int G
 __device__ __forceinline__ int share_owner(long long t, long long T, int G) {
     return int(((t + 1) * G + T - 1) / T) - 1;
 }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+// (a length may come within kTile of 2^31)
+__device__ __forceinline__ int tiles_of(int len) { return int((uint32_t(len) + kTile - 1) / kTile); }
 __device__ __forceinline__ long long item_units(int nt) {
     return nt ? kItemCost + (long long)nt * kTileCost : 0;
 }

@@ -764,6 +764,33 @@ def test_reorder_full_rows_and_bad_indices():
     _no_error()
 
 
+@pytest.mark.parametrize("n_seq", [1, 65])
+def test_attention_lengths_up_to_32_bits(n_seq):
+    """The longest row that a plan takes, 2^31 - 32 tokens, as a sequence of its own or a prefix: its one page
+    over and over, but for the last place. Equal weights give the mean, a large last score the last value."""
+    width, page = (1 << 27) - 2, 16
+    k = torch.zeros((1, 2, 1, page, 64), dtype=F16, device="cuda")
+    v = torch.ones_like(k)
+    v[0, 1, 0, 15] = torch.arange(64, device="cuda") - 20.0
+    k[0, 1, 0, 15, 0] = 40 * 8                      # a score of 40: e^40 is 10^8 times the other weights' sum
+    long = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    long[0, -1] = 1
+    short = torch.zeros((n_seq, 1), dtype=torch.int32, device="cuda")
+    n, none = _ints([width * page]), _ints([0] * n_seq)
+    qq = torch.zeros((n_seq, 1, 64), dtype=F16, device="cuda")
+    out = torch.full_like(qq, math.nan)
+    cache = q.KvCache(k, v)
+    plan = q.AttnPlan(cache, qq, out, short, none, long, n) if n_seq > 1 else q.AttnPlan(cache, qq, out, long, n)
+    plan.execute(0)
+    _no_error()
+    assert ((out - 1).abs() <= 2.0 ** -10).all()
+    qq[..., 0] = 1
+    plan.execute(0)
+    _no_error()
+    e = v[0, 1, 0, 15].double()
+    assert ((out.double() - e).abs() <= 2.0 ** -10 * e.abs() + 2.0 ** -20).all()
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 elements: its last pages are appended to, attended over and copied."""
     n_kv, page, dim = 8, 256, 128
