@@ -104,3 +104,22 @@ def test_beams_stop_at_the_end_token(example):
     for h in hyps:
         if end in h:
             assert all(t == end for t in h[h.index(end):])
+
+
+@pytest.mark.parametrize("at", [0, 2, 4])
+def test_a_finished_beam_keeps_its_score(example, at):
+    """With an end token that the best hypothesis contains, that hypothesis is finished there and only loses
+    to better ones: some hypothesis ends, and the score of each that does is that of its tokens up to the end."""
+    prompt = [1, 2, 3]
+    end = example.beam_search(example.Decoder(seed=3), prompt, 4, 6)[0][0][at]
+    model = example.Decoder(seed=3)
+    hyps, scores = example.beam_search(model, prompt, 4, 12, end=end)
+    assert any(end in h for h in hyps), "no hypothesis ended"
+    assert scores == sorted(scores, reverse=True) and len({tuple(h) for h in hyps}) == 4
+    plain = Plain(model)
+    for h, s in zip(hyps, scores):
+        n = h.index(end) + 1 if end in h else len(h)
+        assert all(t == end for t in h[n:])
+        lp = plain.log_probs(prompt + h[:n])
+        e = sum(float(lp[len(prompt) - 1 + i, t]) for i, t in enumerate(h[:n]))
+        assert abs(s - e) <= PER_TOKEN * n, (s, e)
