@@ -231,7 +231,7 @@ int q2_0_mv_plan_create(const q2_0_mv_desc *descs, int n_desc, int ncols, q2_0_m
     }
     int st = check_device(nullptr);
     if (st != Q2_0_OK) return st;
-    return mv_plan_create(descs, n_desc, ncols, plan);
+    return reported(mv_plan_create(descs, n_desc, ncols, plan));
 }
 
 int q2_0_mv_plan_execute(const q2_0_mv_plan *plan, void *stream) {
@@ -274,7 +274,7 @@ int q2_0_mm_plan_create(const q2_0_mm_desc *descs, int n_desc, int prec, q2_0_mm
     }
     int st = check_device(nullptr);
     if (st != Q2_0_OK) return st;
-    return mm_plan_create(descs, n_desc, prec, plan);
+    return reported(mm_plan_create(descs, n_desc, prec, plan));
 }
 
 int q2_0_mm_plan_execute(const q2_0_mm_plan *plan, void *stream) {
@@ -452,7 +452,7 @@ int q2_0_attn_plan_create(const q2_0_attn_desc *d, q2_0_attn_plan **plan) {
     if (d->width > most || d->prefix_width > most) return Q2_0_EINVAL;
     int st = check_device(nullptr);
     if (st != Q2_0_OK) return st;
-    return attn_plan_create(*d, plan);
+    return reported(attn_plan_create(*d, plan));
 }
 
 int q2_0_attn_plan_execute(const q2_0_attn_plan *plan, int layer, void *stream) {

@@ -12,8 +12,14 @@
 
 namespace q2 {
 
+// A call that failed says so by its own status: the runtime's record of the failure goes, which a
+// later call's check of its launches would take for its own.
+inline int reported(int status) {
+    if (status == Q2_0_ECUDA) cudaGetLastError();
+    return status;
+}
 // Status of the last CUDA call -> q2_0_status.
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? Q2_0_OK : Q2_0_ECUDA; }
+inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? Q2_0_OK : reported(Q2_0_ECUDA); }
 
 // Checks the current device (cached per device): compute capability 10.3.
 int check_device(int *device_out);

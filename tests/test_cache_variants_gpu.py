@@ -1,5 +1,6 @@
 """The decode step's operators in every variant that a plan may take: moving references, launches, captured
 graphs that follow the lengths, and side streams."""
+import ctypes
 import math
 
 import numpy as np
@@ -155,3 +156,19 @@ def test_a_captured_step_of_append_selection_and_reordering():
         for a, b in zip(list(made) + [k, v], want):
             assert torch.equal(a, b), i
     _no_error()
+
+
+def test_a_plan_that_finds_no_memory_leaves_no_error_behind():
+    """Scratch for 65535 sequences of 4096 heads and their prefix does not fit any GPU: the plan is refused, and
+    the next call is not."""
+    k = torch.zeros((1, 1, 64, 16, 128), dtype=F16, device="cuda")
+    cache, some = q.KvCache(k, torch.zeros_like(k)), torch.zeros(64, dtype=F16, device="cuda")
+    ids = torch.zeros(64, dtype=torch.int32, device="cuda")
+    p, i = some.data_ptr(), ids.data_ptr()
+    d = q._AttnDesc(cache._c, p, p, 1, 65535, 4096, 0.1, i, i, 1, i, i, 1)
+    h = ctypes.c_void_p()
+    assert q.lib().q2_0_attn_plan_create(ctypes.byref(d), ctypes.byref(h)) == q.Q2_0_ECUDA and not h.value
+    x = torch.ones((1, 64, 128), device="cuda")
+    q.q2_0_kv_append(cache, 0, None, x, x, None, ids[:1], ids[:1].reshape(1, 1), None)
+    _no_error()
+    assert (k[0, 0, :, 0] == 1).all()
