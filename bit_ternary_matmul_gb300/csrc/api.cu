@@ -395,10 +395,12 @@ int q2_0_quantize_ref(const float *src, void *dst, int64_t nrows, int64_t K, voi
                                        as_stream(stream)));
 }
 
-// A cache struct a call may use: shapes, types, alignment, and rows of `dim`
-// elements that a 32-bit tensor-map coordinate reaches.
+// A cache struct a call may use: shapes, types, alignment, rows of `dim` elements that
+// a 32-bit tensor-map coordinate reaches, and pages whose pieces 32 bits count.
 static bool valid_cache(const q2_0_kv_cache *c) {
-    if (!c || !c->k || !c->v || c->n_pages < 1 || c->n_layers < 1 || c->n_kv < 1) return false;
+    if (!c || !c->k || !c->v || c->n_pages < 1 || c->n_layers < 1 || c->n_kv < 1 ||
+        c->n_kv > (1 << 16))
+        return false;
     if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15u) return false;
     if (c->dim != 64 && c->dim != 128) return false;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return false;
@@ -416,8 +418,7 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_
                    const float *rope, int64_t n_pos, int rot, int style, void *q_out,
                    void *stream) {
     if (!valid_cache(cache) || layer < 0 || layer >= cache->n_layers || n_tokens < 0 ||
-        n_tokens > (int64_t(1) << 31) - 1 || n_q < 0 || n_q > (1 << 16) || cache->n_kv > (1 << 16) ||
-        rot < 0 || rot > cache->dim || rot % 2 ||
+        n_tokens > (int64_t(1) << 31) - 1 || n_q < 0 || n_q > (1 << 16) || rot < 0 || rot > cache->dim || rot % 2 ||
         (style != Q2_0_ROPE_HALVES && style != Q2_0_ROPE_PAIRS))
         return Q2_0_EINVAL;
     if (n_tokens == 0) return Q2_0_OK;

@@ -394,7 +394,7 @@ typedef enum q2_0_rope { Q2_0_ROPE_HALVES = 0, Q2_0_ROPE_PAIRS = 1 } q2_0_rope;
  * place t % page (the same page ids in every layer). The struct is read during
  * the call (or plan_create) it is given to and not kept.
  *   k, v 16-byte aligned; dim 64 or 128; page 16, 32, 64, 128 or 256; type a
- *   q2_0_type; n_layers * n_pages * n_kv * page < 2^31 (byte offsets are 64-bit).
+ *   q2_0_type; n_kv <= 65536, n_layers * n_pages * n_kv * page < 2^31 (byte offsets are 64-bit).
  */
 typedef struct q2_0_kv_cache {
     void *k;
