@@ -659,6 +659,8 @@ class AttnPlan:
         if table.dim() != 2 or table.shape[0] != n:
             raise ValueError("table must be [n_groups * n_seq][width]")
         groups, pw, pt, pl = 1, 0, None, None
+        if prefix_table is None and prefix_len is not None:
+            raise ValueError("prefix_table is needed with prefix_len")
         if prefix_table is not None:
             if prefix_table.dim() != 2 or prefix_table.shape[0] < 1 or n % prefix_table.shape[0]:
                 raise ValueError("prefix_table must be [n_groups][prefix_width]")

@@ -24,3 +24,15 @@ def test_reordering_refuses_more_kv_heads_than_its_counters_hold(L):
     for n_kv in ((1 << 16) + 1, 1 << 19, 1 << 21):
         assert call(n_kv) == q.Q2_0_EINVAL, n_kv
     assert call(1 << 20, 16) == q.Q2_0_EINVAL
+
+
+def test_a_plan_refuses_prefix_lengths_without_their_pages():
+    """They would be passed over, and the sequences would attend to their own tokens alone."""
+    class Cache:
+        k, dim = torch.zeros(1, dtype=torch.float16), 64
+    x = torch.zeros((4, 2, 64), dtype=torch.float16)
+    ids = torch.zeros((4, 1), dtype=torch.int32)
+    with pytest.raises(ValueError, match="prefix_table"):
+        q.AttnPlan(Cache, x, x, ids, ids[:, 0], prefix_len=torch.ones(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):   # (a prefix's table is looked at first)
+        q.AttnPlan(Cache, x, x, ids, ids[:, 0], prefix_table=ids[:1], prefix_len=torch.ones(1, dtype=torch.int32))
