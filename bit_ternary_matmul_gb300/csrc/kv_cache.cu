@@ -54,7 +54,7 @@ __device__ __forceinline__ int64_t token_page(const AppendArgs &a, int64_t t, in
     return p < 0 || p >= a.n_pages ? -2 : p;
 }
 
-// One block per token (and share of its heads, grid.y). A thread owns a unit of
+// One block per token. A thread owns a unit of
 // 16 elements of a head, the same unit of every head it visits, so that the
 // unit's cosines and sines are loaded once: two spans of 8 at (i, i + rot/2), i =
 // 8u, of a rotating unit of HALVES, of 16 neighbours otherwise. Loads are float4,
@@ -65,11 +65,11 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
     const int units = a.dim / 16;
     const int u = threadIdx.x % units;
     const int heads = a.n_q + 2 * a.n_kv;
-    const int step = (128 / units) * gridDim.y;
+    const int step = 128 / units;
     const int slot = a.slot[t];
     const int64_t page = token_page(a, t, slot);
     if (page == -2) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, Q2_0_DEVERR_BAD_ID, t);
+        if (threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_BAD_ID, t);
         return;
     }
     const bool turns = u < a.rot / 16;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
         }
     }
     const int in_page = slot & ((1 << a.page_shift) - 1);
-    for (int h = threadIdx.x / units + (128 / units) * blockIdx.y; h < heads; h += step) {
+    for (int h = threadIdx.x / units; h < heads; h += step) {
         const float *src;
         T *dst;
         const int hk = h - a.n_q;
