@@ -48,12 +48,12 @@
 #include <float.h>
 
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <type_traits>
 
-#include "q2_0_device.cuh"
+#include "q2_0_attn.cuh"
 #include "q2_0_internal.h"
-#include "q2_0_tcgen05.cuh"
 
 namespace q2 {
 
@@ -139,7 +139,7 @@ struct AttnArgs {
     float2 *p_ml, *s_ml;   // their (reference - kLift, sum), a row each; sum 0: nothing
     int grid;
     unsigned long long *err;
-    int stall;  // test hook (q2_0_test_inject_stall): > 0: copies of K end stall - 1 tiles' units into a block's share
+    int stall;  // test hook (q2_0_test_stall_attention): > 0: copies of K end stall - 1 tiles' units into a block's share
 };
 
 // An owner of tiles: a group's prefix (o < n_groups) or a sequence.
@@ -1350,6 +1350,15 @@ namespace {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// Test hook (q2_0_test_stall_attention): 1 + the tiles of the next execute's stall on a device, or 0.
+std::atomic<int> g_stall[64];
+
+int take_stall() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || g_stall[dev] == 0) return 0;
+    return g_stall[dev].exchange(0);
+}
+
 using Kernel = void (*)(AttnArgs);
 struct Variant {
     Kernel fn;
@@ -1482,7 +1491,7 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
 int attn_plan_execute(const q2_0_attn_plan *p, int layer, cudaStream_t s) {
     AttnArgs a = p->args;
     a.row0 = int(layer * p->n_pages);
-    a.stall = take_stall(nullptr);
+    a.stall = take_stall();
     const Variant v = variant_of(p->ncap, p->dim, p->bf);
     // Each launch may be set up while the one before it drains; both wait for its
     // results (griddepcontrol.wait) before they read anything.
@@ -1532,3 +1541,14 @@ void attn_plan_destroy(q2_0_attn_plan *p) {
 }
 
 }  // namespace q2
+
+// Test hook: the next execute on the current device stops copying keys about `tiles` tiles into
+// each block's share, so that the waits for them run out.
+extern "C" int q2_0_test_stall_attention(int tiles) {
+    int dev = 0;
+    if (tiles < 0 || tiles > (1 << 20)) return Q2_0_EINVAL;
+    if (cudaGetDevice(&dev) != cudaSuccess) return q2::reported(Q2_0_ECUDA);
+    if (dev < 0 || dev >= 64) return Q2_0_EUNSUPPORTED;
+    q2::g_stall[dev] = tiles + 1;
+    return Q2_0_OK;
+}

@@ -34,7 +34,6 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <queue>
@@ -1723,10 +1722,21 @@ std::mutex g_attr_mu;
 bool g_t4_attr_done[64];
 
 // Test hook (q2_0_test_inject_stall): a one-shot stall for the next fp4 mat-vec
-// launch or attention execute on a device.
+// launch on a device.
 std::mutex g_stall_mu;
-std::atomic<int> g_stall_stage[64];
+int g_stall_stage[64];
 unsigned long long g_stall_wait_ns[64];
+
+void take_stall(MvParams &prm) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return;
+    std::lock_guard<std::mutex> lk(g_stall_mu);
+    if (g_stall_stage[dev] > 0) {
+        prm.stall_stage = g_stall_stage[dev];
+        prm.wait_ns = g_stall_wait_ns[dev];
+        g_stall_stage[dev] = 0;
+    }
+}
 bool g_s8_attr_done[64][9];
 
 cudaError_t ensure_t4_attr() {
@@ -1848,7 +1858,7 @@ cudaError_t launch_tc(const MvJob &single, const MvParams &prm, int grid, cudaSt
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(prm.ncols == 2 ? T4Lay<kLayBlocks, 2>::kThreads : kTcThreads);
         MvParams prm2 = prm;
-        prm2.stall_stage = take_stall(&prm2.wait_ns);
+        take_stall(prm2);
         if (prm2.layout == kLaySplit) {
             cfg.dynamicSmemBytes = T4Lay<kLaySplit>::kSmem;
             e = cudaLaunchKernelEx(&cfg, mv_t4_kernel<kLaySplit>, single, prm2);
@@ -2242,20 +2252,11 @@ int mv_plan_execute(const q2_0_mv_plan *P, cudaStream_t s) {
     return Q2_0_OK;
 }
 
-int take_stall(unsigned long long *wait_ns) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || g_stall_stage[dev] == 0) return 0;
-    std::lock_guard<std::mutex> lk(g_stall_mu);
-    if (wait_ns) *wait_ns = g_stall_wait_ns[dev];
-    return g_stall_stage[dev].exchange(0);
-}
-
 }  // namespace q2
 
-// Test hook: the next fp4 mat-vec launch (ncols = 1 or 2 on the tensor-core path) or
-// attention execute on the current device stops feeding its pipeline before the given
-// stage (attention: about that many tiles into a block's share), and every pipeline wait of
-// the launch gives up after wait_limit_ns (attention: after the usual second).
+// Test hook: the next fp4 mat-vec launch (ncols = 1 on the tensor-core path) on
+// the current device stops feeding its pipeline before the given stage, and
+// every pipeline wait of that launch gives up after wait_limit_ns.
 extern "C" int q2_0_test_inject_stall(int stage, uint64_t wait_limit_ns) {
     int dev = 0;
     if (stage < 0 || wait_limit_ns == 0 || wait_limit_ns > 10000000000ull) return Q2_0_EINVAL;

@@ -128,23 +128,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, unsign
     }
 }
 
-// As mbar_wait for waits on a critical path: try_wait suspends the thread in hardware
-// until the phase completes or a short time passes, and is simply tried again; the
-// timer, whose read takes longer than most such waits, is looked at from the 64th try on.
-__device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity,
-                                               unsigned long long *err, int tag,
-                                               uint64_t limit_ns = kWaitLimitNs) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > limit_ns) {
-            record_error(err, Q2_0_DEVERR_TIMEOUT, tag);
-            return false;
-        }
-    return true;
-}
-
 // Two or three waits whose phases are usually complete by the time they are
 // checked: the non-blocking tests are all issued before any result is used, so
 // their latencies overlap; a phase not yet complete takes the bounded wait. A
@@ -196,16 +179,6 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *m
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-        : "memory");
-}
-
-// 3-D tiled tensor copy global -> shared; c0 is the innermost coordinate.
-__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int c0, int c1,
-                                            int c2, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
         : "memory");
 }
 

@@ -126,10 +126,6 @@ struct ReorderArgs {
 };
 cudaError_t launch_reorder(const ReorderArgs &a, int64_t n, int n_layers, cudaStream_t s);
 
-// Test hook (q2_0_test_inject_stall): takes the current device's stall; its stage + 1, or 0
-// (*wait_ns is then left as it is).
-int take_stall(unsigned long long *wait_ns);
-
 // attention plans (attn.cu; opaque to the C ABI)
 int attn_plan_create(const q2_0_attn_desc &desc, q2_0_attn_plan **plan);
 int attn_plan_execute(const q2_0_attn_plan *plan, int layer, cudaStream_t s);

@@ -566,13 +566,20 @@ int q2_0_get_error(void *stream, int64_t *info);
  * after wait_limit_ns instead of about one second. The consumers' waits on
  * the missing stage then run out: the kernel records Q2_0_DEVERR_TIMEOUT with
  * info 111 (the wait for a stage's copies), lets the copies it issued land,
- * frees its tensor memory and returns; its outputs are incomplete. Or, if it comes
- * first, the next q2_0_attn_plan_execute does so (info 301 to 314): each block of its
- * attention kernels stops copying keys about `stage` tiles into its share; the waits
- * keep their limit of about a second. Later launches are unaffected. Returns Q2_0_EINVAL for stage < 0 or a limit of 0
+ * frees its tensor memory and returns; its outputs are incomplete. Later
+ * launches are unaffected. Returns Q2_0_EINVAL for stage < 0 or a limit of 0
  * or above 10 s.
  */
 int q2_0_test_inject_stall(int stage, uint64_t wait_limit_ns);
+
+/*
+ * q2_0_test_stall_attention — TEST ONLY, the same for attention: each block of the
+ * next q2_0_attn_plan_execute on the current device stops copying keys about
+ * `tiles` tiles into its share (0: at once), 0 <= tiles <= 2^20. The waits for them
+ * run out after their usual second, Q2_0_DEVERR_TIMEOUT is recorded with info 301 to
+ * 314, and the outputs are incomplete.
+ */
+int q2_0_test_stall_attention(int tiles);
 
 #ifdef __cplusplus
 }

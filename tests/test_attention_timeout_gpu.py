@@ -1,4 +1,4 @@
-"""The attention kernels' waits are bounded: q2_0_test_inject_stall makes every block of one execute stop
+"""The attention kernels' waits are bounded: q2_0_test_stall_attention makes every block of one execute stop
 copying keys some tiles into its share. The waits run out (after a second), the execute records
 Q2_0_DEVERR_TIMEOUT (info 301 to 314), the join that follows it stays inside the plan's scratch, whatever
 that memory held before the plan, and the next executes are correct."""
@@ -42,7 +42,7 @@ def test_stalled_attention_times_out_and_recovers(plens, lens, n_q, n_kv, dim, d
     del dirt
     torch.cuda.empty_cache()        # a new plan's scratch may be this memory
     plan = c.plan()
-    q.q2_0_test_inject_stall(stage, 2_000_000)
+    q.q2_0_test_stall_attention(stage)
     t0 = time.perf_counter()
     plan.execute(0)
     code, info = q.q2_0_get_error()     # synchronises
@@ -54,7 +54,7 @@ def test_stalled_attention_times_out_and_recovers(plens, lens, n_q, n_kv, dim, d
         assert q.q2_0_get_error() == (0, 0)
         c.check("after the stall")
     if stage == 2:      # now with an earlier execute's records
-        q.q2_0_test_inject_stall(stage, 2_000_000)
+        q.q2_0_test_stall_attention(stage)
         plan.execute(0)
         code, info = q.q2_0_get_error()
         assert code == q.Q2_0_DEVERR_TIMEOUT and 301 <= info <= 314, (code, info)
