@@ -35,15 +35,15 @@
 //   bandwidth with the copies; here 64 KB per 128 rows and P not at all.
 //
 // Measured on one GB300 (device time of an execute, in a graph; floors at its 6.7 TB/s
-// copy): 4 beams, 517 shared and 37 own tokens, 16 / 8 heads of 128: 11.0 us (latency:
+// copy): 4 beams, 517 shared and 37 own tokens, 16 / 8 heads of 128: 11.3 us (latency:
 // clocks read in an earlier version gave 2 us to the deal and 3 to 5 more to the first
-// scores). 8 beams, 50021 + 200, 32 / 8 heads of 128: 43.6 us, floor 31.6 (the same clocks:
+// scores). 8 beams, 50021 + 200, 32 / 8 heads of 128: 44.4 us, floor 31.6 (the same clocks:
 // first scores 6 to 8 us after the deal, with all blocks' first tiles in flight). 4 x 16
-// sequences, up to 4099 + 1500, 16 heads of 64: 53.4 us, floor 37.4 (the same clocks: about
+// sequences, up to 4099 + 1500, 16 heads of 64: 55.8 us, floor 37.4 (the same clocks: about
 // 4000 to end a segment, 1200 to 1700 of work a tile). 64 sequences, 131072 + up to 3000,
-// 32 / 8 heads of 128: 192 us, floor 139. Profiled one by one with cold caches,
-// attn_rows_kernel takes 128 us of it (tensor pipe 48 % busy, memory 53 %: neither is full)
-// and attn_kernel 72 (memory 73 %).
+// 32 / 8 heads of 128: 190 us, floor 139. Profiled one by one with cold caches,
+// attn_rows_kernel takes 123 us of it (tensor pipe 48 % busy, memory 56 %: neither is full)
+// and attn_kernel 72 (memory 74 %).
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -70,8 +70,8 @@ constexpr float kLift = 7.0f;  // p = 2^(s - ref + kLift)
 constexpr float kSlack = 8.0f; // how far a score may pass the reference
 constexpr float kFused = 1.6e7f; // references up to which a score is scaled and reduced by it in one operation
 // Cost of a tile, and of a segment beside its tiles, for the shares. Measured (four groups of
-// sixteen, 4099 shared and up to 1500 own tokens, dim 64): 4 of an item 60.5 us, 8 55.9, 14 53.4,
-// 20 54.3, 28 58.8; at dim 128 it hardly matters.
+// sixteen, 4099 shared and up to 1500 own tokens, dim 64): 4 of an item 64.0 us, 8 59.3, 14 55.3,
+// 20 55.9, 28 59.3; 8 beams on 50021 tokens of dim 128 43.6 to 44.2 with any of them.
 constexpr int kTileCost = 4, kItemCost = 14;
 
 // Sizes of a variant of attn_kernel: NCAP, 32 or 64, is the most query rows of a product.
@@ -1418,7 +1418,13 @@ int attn_plan_create(const q2_0_attn_desc &d, q2_0_attn_plan **plan) {
     a.grid = sms;
     a.err = err;
     a.stall = 0;
-    // More than 64 rows to a prefix: 128 or 256 at a time by attn_rows_kernel.
+    // More than 64 rows to a prefix: 128 or 256 at a time by attn_rows_kernel. Lengths are not known here,
+    // so that rows alone decide. Measured with 8 kv heads of 128 on 4099 and on 50021 keys (us), blocks of 64
+    // rows by attn_kernel against attn_rows_kernel: 48 rows 19 and 54 against 25 and 58, 64 rows 20 and 55
+    // against 26 and 59, 96 rows 23 and 76 against 30 and 63, 128 rows 26 and 65 against 32 and 65; heads of
+    // 64: 64 rows 19 and 45 against 23 and 47, 96 rows 22 and 60 against 25 and 50, 128 rows 25 and 61 against 25
+    // and 51. Above 128 rows, 128 at a time against 256: 160 rows 33 and 96 against 33 and 72, heads of 64 28 and 66
+    // against 29 and 65; up to 128 rows the smaller tile is ahead by 0 to 2 %.
     const int64_t rows = d.prefix_width ? d.n_seq * a.share : a.share;
     p->by_rows = !d.prefix_width || rows <= 64 ? 0 : rows <= 128 ? 128 : 256;
     p->ncap = (p->by_rows ? a.share : rows) <= 32 ? 32 : 64;

@@ -10,8 +10,8 @@
 //
 // Measured on one GB300 (device time; 151936 logits a row, 6.7 TB/s copy): 4 rows
 // 8.3 us, 64 rows 19, 256 rows 39 (156 MB: 23 at the copy rate), 800 rows 89
-// (5.4 TB/s). At 256 rows, profiled with cold caches, pass 1 takes 37 us (memory
-// 50 % busy) and pass 2 9.6. What is over the copy rate is put down to the rankings of
+// (5.4 TB/s). At 256 rows, profiled with cold caches, pass 1 takes 36 us (memory
+// 51 % busy) and pass 2 9.8. What is over the copy rate is put down to the rankings of
 // each chunk's first and last piece, in which a block does not stream, and to pass 2;
 // their shares were not measured apart.
 #include <float.h>
@@ -653,8 +653,10 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // Chunks of a row: the number with the least time, in units of a piece's share of the
 // memory rate of an SM (0.37 us): a block's own time is about 16 units and 2 a piece, in
 // waves of kBlocks1 per SM, and the busiest SM's pieces have to be read. Measured at
-// 151936 logits, 8 chosen: 64 rows in 7 chunks 19.1 us, in 8 21.2; 256 rows in 1 38.4,
-// in 2 40.5, in 7 43.5.
+// 151936 logits, 8 chosen, the rule's choice first: 4 rows in 38 chunks 8.5 us, in 19 9.0, in 8
+// 11.1; 64 rows in 7 19.4, in 4 20.5, in 8 22.9, in 1 27.6; 256 rows in 3 40.4, in 1 38.4, in 2 44.1, in 7
+// 47.7 (16 chosen: in 3 45.5, in 1 41.0). So at 256 rows it misses the best by 5 to 11 %; how many
+// are chosen is not in it.
 int chunks_of(size_t rows, int pieces) {
     int best = 1;
     size_t best_cost = ~size_t(0);

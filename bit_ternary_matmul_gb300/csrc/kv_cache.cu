@@ -4,7 +4,7 @@
 //
 // Both are bound by memory: append reads 4 bytes and writes 2 per value, reorder
 // reads and writes 2. Measured on one GB300 against its 6.7 TB/s copy: 16384 tokens of
-// 32 + 8 + 8 heads of 128 (613 MB) appended in 96 us, 6.4 TB/s; 8 tokens of 16 + 8 + 8
+// 32 + 8 + 8 heads of 128 (613 MB) appended in 94.3 us, 6.5 TB/s; 8 tokens of 16 + 8 + 8
 // heads in 2.5 us; the last pages of 128 beams in 36 layers reordered in 87.8 us (profiled
 // cold: 84, memory 69 % busy), of 8 beams in 28 layers in 4.3 us.
 #include <cuda_bf16.h>
@@ -54,11 +54,11 @@ __device__ __forceinline__ int64_t token_page(const AppendArgs &a, int64_t t, in
     return p < 0 || p >= a.n_pages ? -2 : p;
 }
 
-// One block per token. A thread owns a unit of
-// 16 elements of a head, the same unit of every head it visits, so that the
-// unit's cosines and sines are loaded once: two spans of 8 at (i, i + rot/2), i =
-// 8u, of a rotating unit of HALVES, of 16 neighbours otherwise. Loads are float4,
-// stores 16 bytes; the inputs are read once (streaming loads).
+// One block per token. A thread owns a unit of 16 elements of a head, the same
+// unit of every head it visits, so that the unit's cosines and sines are loaded
+// once: two spans of 8 at (i, i + rot/2), i = 8u, of a rotating unit of HALVES, of
+// 16 neighbours otherwise. Loads are float4, stores 16 bytes; the inputs are read
+// once (streaming loads).
 template <typename T>
 __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
     const int64_t t = blockIdx.x;

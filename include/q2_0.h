@@ -412,7 +412,7 @@ typedef struct q2_0_kv_cache {
  * v in one layer of the cache.
  *   q, k, v   F32, token t's heads [n_q or n_kv][dim] at q + t * q_stride (strides
  *             in floats, >= heads * dim; so the three may be slices of one
- *             product's rows). q and q_out may be NULL with n_q = 0.
+ *             product's rows). n_q <= 65536; q and q_out may be NULL with n_q = 0.
  *   pos       int32 [n_tokens], the row of `rope` that turns the token.
  *   slot      int32 [n_tokens], the token's place in its sequence's row of
  *             `table`; a negative slot stores nothing (padding), q is still
@@ -447,7 +447,7 @@ int q2_0_kv_append(const q2_0_kv_cache *cache, int layer, const float *q, int64_
  *   not end with a page: the places past a length are never used, whatever
  *   they hold.
  *   q, out    [n_groups * n_seq][n_q][dim] in the cache's type, 16-byte aligned;
- *             n_q a multiple of n_kv, n_q / n_kv <= 64; n_groups * n_seq <= 65535,
+ *             n_q a multiple of n_kv, <= 65535, n_q / n_kv <= 64; n_groups * n_seq <= 65535,
  *             n_groups * n_seq * n_q <= 2^28.
  *   prefix_table int32 [n_groups][prefix_width], prefix_len int32 [n_groups]:
  *             both NULL with prefix_width = 0 where nothing is shared.
@@ -512,7 +512,7 @@ void q2_0_attn_plan_destroy(q2_0_attn_plan *plan);
  * the larger logit, then the lower token.
  *   score_out, parent, token   F32, int32, int32 [n_groups][n_out]. Where fewer
  *             than n_out continuations are possible the rest have score -inf,
- *             parent 0 and token -1.
+ *             parent 0 and token -1. They must not overlap the inputs.
  *   1 <= n_beams <= 64, 1 <= n_out <= 32, 1 <= n_vocab < 2^31 - 2^16,
  *   n_groups * n_beams <= 65535. n_groups == 0 is a no-op.
  * workspace: at least q2_0_beam_select_workspace_size(...) bytes of device
