@@ -582,12 +582,13 @@ int q2_0_draft_verify(const float *target, int64_t target_stride, const float *d
                                      n_seq, n_draft, n_vocab, accepted, token, err, as_stream(stream)));
 }
 
-// Rows of a valid cache, and where their outcome goes: each array itself, or one apart from all of `r`.
+// Rows of a valid cache, and where their outcome goes: each array itself, or one apart from all of `r` and from the others of
+// the outcome. (What is read of the arrays is checked once: it must not change while a call is at work.)
 static bool valid_rows(const q2_0_kv_cache *c, const q2_0_kv_rows *r, const q2_0_kv_rows *out) {
     if (!r || !r->refs || !r->table || !r->len || r->n_rows < 1 || r->n_rows > (1 << 20) || r->width < 1 ||
         r->width > ((int64_t(1) << 31) - 1) / c->page)
         return false;
-    if (!out) return true;
+    if (!out) out = r;
     if (!out->refs || !out->table || !out->len || out->n_rows != r->n_rows || out->width != r->width) return false;
     const int64_t bytes[3] = {c->n_pages * 4, r->n_rows * r->width * 4, r->n_rows * 4};
     const int32_t *const from[3] = {r->refs, r->table, r->len}, *const to[3] = {out->refs, out->table, out->len};
@@ -595,6 +596,7 @@ static bool valid_rows(const q2_0_kv_cache *c, const q2_0_kv_rows *r, const q2_0
         for (int j = 0; j < 3; ++j) {
             if (i == j && from[i] == to[i]) continue;
             if (overlap(to[i], bytes[i], from[j], bytes[j])) return false;
+            if (i < j && (overlap(from[i], bytes[i], from[j], bytes[j]) || overlap(to[i], bytes[i], to[j], bytes[j]))) return false;
         }
     return true;
 }

@@ -203,6 +203,37 @@ def test_compact_refusals(L):
         _passes(call, **over)
 
 
+def _calls_on_rows(L):
+    """(name, call) of every call on rows, with arguments that are accepted."""
+    far = Q + (1 << 20)
+    return [("fork", lambda r, out=None: L.q2_0_kv_fork(_ref(_cache(k=far, v=far)), _ref(r), Q, Q, 2, _ref(out), None)),
+            ("resize", lambda r, out=None: L.q2_0_kv_resize(_ref(_cache(k=far, v=far)), _ref(r), Q, _ref(out), None, 0, None)),
+            ("compact", lambda r, out=None: L.q2_0_kv_compact(_ref(_cache(k=far, v=far)), _ref(r), _ref(out), Q, Q + 64, None, 0, None))]
+
+
+def test_rows_whose_arrays_overlap_one_another_are_refused(L):
+    """Of rows before a call, and of two new arrays for their outcome: 40 bytes of counts, 48 of a table, 16 of lengths."""
+    bad = [dict(refs=P, table=P), dict(refs=P, len=P), dict(table=P, len=P), dict(refs=P, table=P + 36), dict(refs=P, table=P - 44),
+           dict(refs=P, len=P + 36), dict(refs=P, len=P - 12), dict(table=P, len=P + 44), dict(table=P, len=P - 12)]
+    good = [dict(refs=P, table=P + 40), dict(refs=P, table=P - 48), dict(refs=P, len=P + 40), dict(refs=P, len=P - 16),
+            dict(table=P, len=P + 48), dict(table=P, len=P - 16), dict(refs=P, table=P + 40, len=P + 88)]
+    far = 1 << 18
+
+    def at(over, by=0):
+        f = {n: P + (i + 5) * 4096 for i, n in enumerate(("refs", "table", "len"))}
+        f.update(over)
+        return {n: x + by for n, x in f.items()}
+    for name, call in _calls_on_rows(L):
+        for over in bad:
+            assert call(_rows(**at(over))) == EINVAL, (name, over)                      # in place
+            assert call(_rows(**at(over)), _rows(**at(over))) == EINVAL, (name, over)
+            assert call(_rows(), _rows(**at(over, far))) == EINVAL, (name, over)        # new arrays
+            assert call(_rows(**at(over)), _rows(**at({}, far))) == EINVAL, (name, over)
+        for over in good:
+            _passes(lambda r: call(r), r=_rows(**at(over)))
+            _passes(lambda out: call(_rows(), out), out=_rows(**at(over, far)))
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     f, i = torch.zeros((2, 3, 5)), torch.zeros((2, 2), dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
