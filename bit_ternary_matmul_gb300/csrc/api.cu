@@ -605,20 +605,26 @@ static bool apart(const void *p, int64_t bytes, const q2_0_kv_cache *c, const q2
     return !overlap(p, bytes, out.refs, c->n_pages * 4) && !overlap(p, bytes, out.table, out.n_rows * out.width * 4) &&
            !overlap(p, bytes, out.len, out.n_rows * 4);
 }
+// Whether an array of `bytes` shares memory with the cache's pages.
+static bool in_cache(const void *p, int64_t bytes, const q2_0_kv_cache *c) {
+    const int64_t cache = c->n_pages * c->n_layers * c->n_kv * c->page * c->dim * 2;
+    return overlap(p, bytes, c->k, cache) || overlap(p, bytes, c->v, cache);
+}
 // A workspace that a call on rows can take: large enough, aligned, beside the rows and the cache.
 static bool valid_rows_workspace(const void *ws, size_t bytes, size_t need, const q2_0_kv_cache *c, const q2_0_kv_rows &r,
                                  const q2_0_kv_rows &out) {
     if (!ws) return true;
-    const int64_t n = int64_t(need), cache = c->n_pages * c->n_layers * c->n_kv * c->page * c->dim * 2;
+    const int64_t n = int64_t(need);
     return bytes >= need && !(reinterpret_cast<uintptr_t>(ws) & 255u) && apart(ws, n, c, r) && apart(ws, n, c, out) &&
-           !overlap(ws, n, c->k, cache) && !overlap(ws, n, c->v, cache);
+           !in_cache(ws, n, c);
 }
 
 int q2_0_kv_copy(const q2_0_kv_cache *cache, const int32_t *src, const int32_t *dst, const int32_t *count, int64_t n,
                  void *stream) {
     if (!valid_cache(cache) || n < 0 || n > (int64_t(1) << 31) - 1) return Q2_0_EINVAL;
     if (n == 0) return Q2_0_OK;
-    if (!src || !dst) return Q2_0_EINVAL;
+    if (!src || !dst || in_cache(src, n * 4, cache) || in_cache(dst, n * 4, cache) || in_cache(count, n * 4, cache))
+        return Q2_0_EINVAL;
     int st = check_device(nullptr);
     if (st != Q2_0_OK) return st;
     unsigned long long *err = error_word_ptr();
@@ -679,7 +685,8 @@ int q2_0_kv_compact(const q2_0_kv_cache *cache, const q2_0_kv_rows *rows, const 
     const q2_0_kv_rows &out = rows_out ? *rows_out : *rows;
     for (const q2_0_kv_rows *r : {rows, &out})
         if (!apart(place, cache->n_pages * 4, cache, *r) || !apart(live, 4, cache, *r)) return Q2_0_EINVAL;
-    if (overlap(place, cache->n_pages * 4, live, 4)) return Q2_0_EINVAL;
+    if (overlap(place, cache->n_pages * 4, live, 4) || in_cache(place, cache->n_pages * 4, cache) || in_cache(live, 4, cache))
+        return Q2_0_EINVAL;
     const size_t need = compact_workspace_bytes(cache->n_pages);
     if (!valid_rows_workspace(workspace, workspace_bytes, need, cache, *rows, out) ||
         overlap(workspace, int64_t(need), place, cache->n_pages * 4) ||

@@ -648,9 +648,11 @@ int q2_0_draft_verify(const float *target, int64_t target_stride, const float *d
  *   1 <= n_rows <= 2^20, 1 <= width, width * page < 2^31.
  * rows_out is where a call leaves its outcome: NULL or the same arrays, in place; or
  * other arrays of the same sizes that overlap nothing, e.g. while attention in
- * flight still reads the old ones (each of the three by itself). A call's other
- * arrays and its workspace must not overlap those that it writes, nor a workspace
- * the cache. Calls on the same rows, pages or workspace must not overlap on the GPU.
+ * flight still reads the old ones (each of the three by itself). The three arrays
+ * must not overlap one another, and a call's other arrays and its workspace not
+ * those that it writes, nor the cache's pages where a call writes these or the
+ * array: Q2_0_EINVAL. Rows must not lie in the cache's pages either (that is not
+ * checked). Calls on the same rows, pages or workspace must not overlap on the GPU.
  */
 typedef struct q2_0_kv_rows {
     int32_t *refs;
@@ -665,7 +667,7 @@ typedef struct q2_0_kv_rows {
  * values: their first count[i] tokens (NULL: all of them).
  *   src, dst, count  int32 [n]. A page may be copied to several, but must be the
  *   destination of one copy at most, and not a source as well. A negative src[i]
- *   copies nothing (padding).
+ *   copies nothing (padding). The arrays must not lie in the cache's pages.
  * A page id outside [0, n_pages) or a count outside [0, page] copies nothing and
  * records Q2_0_DEVERR_BAD_ID with info = i. n == 0 is a no-op; n < 2^31.
  */
@@ -720,7 +722,7 @@ int q2_0_kv_resize(const q2_0_kv_cache *cache, const q2_0_kv_rows *rows, const i
  * to the next, until all lie below n, in all layers; refs and table follow.
  *   place  int32 [n_pages], written: where each page of before is now, -1 for free
  *          ones (for tables of the caller's own).
- *   live   int32 [1], written: n.
+ *   live   int32 [1], written: n. Neither may lie in the cache's pages.
  * A length outside [0, width * page] leaves its row's table as it is, and a page id
  * outside [0, n_pages) its place; both record Q2_0_DEVERR_BAD_ID with info = the row.
  * workspace: at least q2_0_kv_compact_workspace_size(n_pages, n_rows) bytes, 256-byte

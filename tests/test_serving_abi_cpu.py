@@ -205,10 +205,10 @@ def test_compact_refusals(L):
 
 def _calls_on_rows(L):
     """(name, call) of every call on rows, with arguments that are accepted."""
-    far = Q + (1 << 20)
-    return [("fork", lambda r, out=None: L.q2_0_kv_fork(_ref(_cache(k=far, v=far)), _ref(r), Q, Q, 2, _ref(out), None)),
-            ("resize", lambda r, out=None: L.q2_0_kv_resize(_ref(_cache(k=far, v=far)), _ref(r), Q, _ref(out), None, 0, None)),
-            ("compact", lambda r, out=None: L.q2_0_kv_compact(_ref(_cache(k=far, v=far)), _ref(r), _ref(out), Q, Q + 64, None, 0, None))]
+    c = _cache(k=Q + (1 << 20), v=Q + (1 << 20))
+    return [("fork", lambda r, out=None: L.q2_0_kv_fork(_ref(c), _ref(r), Q, Q, 2, _ref(out), None)),
+            ("resize", lambda r, out=None: L.q2_0_kv_resize(_ref(c), _ref(r), Q, _ref(out), None, 0, None)),
+            ("compact", lambda r, out=None: L.q2_0_kv_compact(_ref(c), _ref(r), _ref(out), Q, Q + 64, None, 0, None))]
 
 
 def test_rows_whose_arrays_overlap_one_another_are_refused(L):
@@ -232,6 +232,26 @@ def test_rows_whose_arrays_overlap_one_another_are_refused(L):
         for over in good:
             _passes(lambda r: call(r), r=_rows(**at(over)))
             _passes(lambda out: call(_rows(), out), out=_rows(**at(over, far)))
+
+
+def test_numbers_in_the_pages_that_a_call_writes_are_refused(L):
+    """Keys of 81920 bytes at P, values behind a gap."""
+    k, v, far = P, P + (1 << 18), P + (1 << 19)
+    c, r = _cache(k=k, v=v), _rows(refs=far + 4096, table=far + 8192, len=far + 12288)
+
+    def copy(src=far, dst=far + 64, count=far + 128):
+        return L.q2_0_kv_copy(_ref(c), src, dst, count, 3, None)
+
+    def compact(place=far, live=far + 64):
+        return L.q2_0_kv_compact(_ref(c), _ref(r), None, place, live, None, 0, None)
+    for call, sizes in ((copy, dict(src=12, dst=12, count=12)), (compact, dict(place=40, live=4))):
+        for name, size in sizes.items():
+            for base in (k, v):
+                for p in (base, base - size + 4, base + 81920 - 4):
+                    assert call(**{name: p}) == EINVAL, (name, p)
+                for p in (base - size, base + 81920):
+                    _passes(call, **{name: p})
+    _passes(copy, count=None)
 
 
 def test_binding_refuses_tensors_that_do_not_fit():
