@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const __gri
     const int stand = stand_s;
     if (stand < 0) {  // (all blocks of the cluster come to the same)
         if (rank == 0 && threadIdx.x == 0) record_error(a.err, Q2_0_DEVERR_BAD_ID, b);
+        __syncwarp();  // (the cluster's barrier takes a warp's lanes together)
         cluster_wait();
         return;
     }
