@@ -647,12 +647,16 @@ int q2_0_draft_verify(const float *target, int64_t target_stride, const float *d
  * refs true to the table.
  *   1 <= n_rows <= 2^20, 1 <= width, width * page < 2^31.
  * rows_out is where a call leaves its outcome: NULL or the same arrays, in place; or
- * other arrays of the same sizes that overlap nothing, e.g. while attention in
- * flight still reads the old ones (each of the three by itself). The three arrays
- * must not overlap one another, and a call's other arrays and its workspace not
- * those that it writes, nor the cache's pages where a call writes these or the
- * array: Q2_0_EINVAL. Rows must not lie in the cache's pages either (that is not
- * checked). Calls on the same rows, pages or workspace must not overlap on the GPU.
+ * other arrays of the same sizes that overlap nothing (each of the three by itself),
+ * e.g. while attention in flight still reads the old ones, and what their rows hold
+ * in the cache: q2_0_kv_fork writes no page, q2_0_kv_compact only pages that were
+ * free. q2_0_kv_resize also writes pages that are given back in it: attention on old
+ * rows that give pages back has to end before the call, on others it may go on.
+ * The three arrays must not overlap one another, and a call's other arrays and its
+ * workspace not those that it writes, nor the cache's pages where a call writes
+ * these or the array: Q2_0_EINVAL. Rows must not lie in the cache's pages either
+ * (that is not checked). The calls below must not overlap one another on the GPU
+ * where they have rows, pages or a workspace in common.
  */
 typedef struct q2_0_kv_rows {
     int32_t *refs;
