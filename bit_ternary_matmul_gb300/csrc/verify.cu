@@ -10,9 +10,12 @@
 //
 // Sums are pairs of floats, the sum and what it lost (two-sum: 6 additions a value, two values at once by
 // the packed f32x2 forms): one addition in f64 would take 64 times an f32 one's share of the SM. A pair's second
-// part is rounded to 2^-24 of itself at each addition: over n additions at most n^2 2^-48 of the sum, n <= 64
-// before a pair is added to another and settled (which rounds by 2^-46): 2^-36 for the values of one such pair at worst,
-// and 2^-42 as roundings go.
+// part, up to j 2^-24 of the sum after j additions, is rounded to 2^-24 of itself at each: (n^2 + n) / 2 units of 2^-48 of the
+// sum over n additions at worst. So n is 16 before a pair is added to that of all such windows, which is settled (136 units,
+// 33 for the addition and 3 for each window before it; with n = 64 it would be 2080, more than 2^-37). A warp's sum takes
+// 38 units, the running sums over the runs, the parts of one and its tokens 511 and 3 for each 8192 tokens: together with
+// the windows' (half of a run's error goes into the total as well) below 2^-38 + n_vocab 2^-58 of the total where a running
+// sum is compared with r * total.
 //
 // Measured in a CUDA graph, inputs beyond L2: 3 drafts of 1 sequence over 151936 tokens 6.4 us (1.2 MB: the bytes take 0.2, a
 // sequence of dependent reads, barriers and prefix sums the rest: 1000 tokens take 5.7), 64 sequences 16.7 (67 MB at
@@ -32,7 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRuns = kMaxCluster * kWarps;
-constexpr int kFlush = 8;   // times 16 values that two pairs take before they are added to another
+constexpr int kFlush = 2;   // times 16 values that two pairs take before they are added to another
 constexpr int kResident = 4;      // blocks of an SM
 constexpr int kMinBlock = 2048;  // values of a block, and where SMs have several
 constexpr int kMinShare = 8000;
@@ -118,6 +121,14 @@ __device__ __forceinline__ void add(Pair2 &p, uint64_t w) {
     p.l = add2(p.l, add2(sub2(p.h, sub2(s, b)), sub2(w, b)));
     p.h = s;
 }
+// A window's pairs go to those of all windows, which are settled again.
+__device__ __forceinline__ void flush(Pair2 &all, Pair2 &p) {
+    const uint64_t s = add2(all.h, p.h), b = sub2(s, all.h);
+    const uint64_t l = add2(add2(sub2(all.h, sub2(s, b)), sub2(p.h, b)), add2(all.l, p.l));
+    all.h = add2(s, l);
+    all.l = sub2(l, sub2(all.h, s));
+    p = {0, 0};
+}
 
 // What counts as a probability: not a negative one or NaN.
 __device__ __forceinline__ float clean(float p) { return fmaxf(p, 0.0f); }
@@ -138,7 +149,6 @@ struct Row {
 // 16 values of each row on their way at a time.
 template <bool kQ>
 __device__ __forceinline__ Pair run_sum(const Row &row, int v0, int v1, bool wide, int lane) {
-    Pair sum = {0.0f, 0.0f};
     int v = v0;
     auto take = [&](Pair2 &s, float4 p, float4 q, int out) {  // out: where row.out is among them
         p = make_float4(clean(p.x), clean(p.y), clean(p.z), clean(p.w));
@@ -153,7 +163,7 @@ __device__ __forceinline__ Pair run_sum(const Row &row, int v0, int v1, bool wid
         add(s, pack(p.z, p.w));
     };
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    Pair2 s = {0, 0};
+    Pair2 sum = {0, 0}, s = {0, 0};
     int taken = 0;
     if (wide) {
         const int whole = v0 + (v1 - v0) / 4 * 4;
@@ -167,10 +177,7 @@ __device__ __forceinline__ Pair run_sum(const Row &row, int v0, int v1, bool wid
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) take(s, p[k], kQ ? q[k] : zero, row.out - (v + 128 * k + 4 * lane));
-            if (++taken % kFlush == 0) {
-                sum = settled(sum + s.sum());
-                s = {0, 0};
-            }
+            if (++taken % kFlush == 0) flush(sum, s);
         }
         v = whole;
     }
@@ -186,12 +193,10 @@ __device__ __forceinline__ Pair run_sum(const Row &row, int v0, int v1, bool wid
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
             take(s, make_float4(p[k], p[k + 1], p[k + 2], p[k + 3]), kQ ? make_float4(q[k], q[k + 1], q[k + 2], q[k + 3]) : zero, -1);
-        if (++taken % kFlush == 0) {
-            sum = settled(sum + s.sum());
-            s = {0, 0};
-        }
+        if (++taken % kFlush == 0) flush(sum, s);
     }
-    return settled(warp_sum(settled(sum + s.sum())));
+    flush(sum, s);
+    return settled(warp_sum(settled(sum.sum())));
 }
 __device__ __forceinline__ Pair run_sum(const Row &row, int v0, int v1, bool wide, int lane) {
     return row.q ? run_sum<true>(row, v0, v1, wide, lane) : run_sum<false>(row, v0, v1, wide, lane);

@@ -617,10 +617,10 @@ int q2_0_moe_route(const q2_0_router *router, const float *logits, int64_t strid
  * rejected token left out), else from w = p of row count[b]: the first token with
  * w > 0 whose running sum exceeds r * total, r the last number of rand; the last
  * token with w > 0 if none does. Where all w are 0 it is drawn from p; where that
- * is all 0 too it is -1. Running sums are held to 2^-38 of the total, and
- * r * total to 2^-149. A negative probability and NaN count as 0; rows need not sum to
- * 1, but their sums have to be finite in f32 (otherwise any token of the row, or -1,
- * is drawn).
+ * is all 0 too it is -1. Running sums are held, and compared with r * total, to
+ * within 2^-38 + n_vocab * 2^-58 of the total, and 2^-149. A negative probability and
+ * NaN count as 0; rows need not sum to 1, but their sums have to be finite in f32
+ * (otherwise any token of the row, or -1, is drawn).
  *   accepted int32 [n_seq].   token  int32 [n_seq][n_draft + 1]: the drafts that
  *   stand, the next token, then -1. They must not overlap the inputs or
  *   each other.
