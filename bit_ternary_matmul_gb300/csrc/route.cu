@@ -71,9 +71,16 @@ __device__ __forceinline__ T warp_sum(T v) {
 // Group of expert e < 1024 for groups of `size` (>= 1): exact, as e * size < 2^22.
 __device__ __forceinline__ int group_of(int e, uint32_t inv) { return int((uint32_t(e) * inv) >> 22); }
 
+// A group's score of its two highest keys: the highest, or half the sum of both (a sum of two may be beyond f32; without
+// a second one, -inf, half the first).
+template <typename T>
+__device__ __forceinline__ T group_score(T a, T b, bool two) {
+    return two ? T(0.5) * a + (b > T(-INFINITY) ? T(0.5) * b : T(0)) : a;
+}
+
 // The groups that are chosen from, as a mask: g's sum of its `top` highest keys (in `key`, this
 // warp's copy of the row) is among the n_group_used highest. T float or double. *near is set
-// where two of them that the choice parts are closer than `margin`.
+// where two scores that the choice parts are closer than `margin`.
 template <typename T>
 __device__ uint32_t best_groups(const T *key, const q2_0_router &r, int top, T margin, bool *near) {
     const int lane = threadIdx.x & 31;
@@ -106,7 +113,7 @@ __device__ uint32_t best_groups(const T *key, const q2_0_router &r, int top, T m
             b = b > a2 ? b : a2;
         }
     }
-    const T score = top == 2 && b > T(-INFINITY) ? a + b : a;
+    const T score = group_score(a, b, top == 2);
     int rank = 0;
     for (int h = 0; h < r.n_group; ++h) {
         const T other = __shfl_sync(~0u, score, h * sub);
@@ -415,6 +422,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<kW, kE>) route_kernel(
         float margin = 0.0f;
         if (kBias || sums) margin = softmax ? float(per + 32) * 0x1p-23f * inv_z : 0x1p-20f;
         if (kBias) margin += 0x1p-22f * (1.0f + most);
+        const float group_margin = r.group_top == 2 ? margin : 2.0f * margin;  // (of half a sum of two: half of two keys')
         bool full = false, in = true;  // full: the whole row has to be ranked in 64 bits
         if (kGrouped && !lanes) {
             __syncwarp();
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<kW, kE>) route_kernel(
             for (int h = 0; h < kRows; ++h) {
                 bool near;
                 const uint32_t s = best_groups<float>(warp_s + h * kFloats<kW, kE>, r, r.group_top,
-                                                      __shfl_sync(~0u, 2.0f * margin, h * kW), &near);
+                                                      __shfl_sync(~0u, group_margin, h * kW), &near);
                 if (h == row) {
                     set = s;
                     full = near;
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<kW, kE>) route_kernel(
                 b = fmaxf(fmaxf(b, b2), fminf(a, a2));
                 a = fmaxf(a, a2);
             }
-            const float score = r.group_top == 2 && b > -INFINITY ? a + b : a;
+            const float score = group_score(a, b, r.group_top == 2);
             const int g = in_row >> shift;
             float left = g < r.n_group ? score : -INFINITY, lowest = 0.0f;
             in = false;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident<kW, kE>) route_kernel(
             }
             full = lowest == -INFINITY;  // groups of masked experts alone: which are taken is seen to below
             const float highest = row_max<kW>(left);
-            const bool near = margin > 0.0f && highest > -INFINITY && lowest - highest < 2.0f * margin;
+            const bool near = margin > 0.0f && highest > -INFINITY && lowest - highest < group_margin;
             if (__any_sync(~0u, near)) {
                 double m64 = 0, z64 = 1;
                 if (softmax)
