@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kWarps = 4;           // of a block
 constexpr int kTwoExperts = 160;    // most experts of a row that has half a warp
+static_assert(kTwoExperts <= 16 * 16, "");
 constexpr int kTwoTokens = 8;       // and least rows an SM
 constexpr float kMax = 3.402823466e38f;
 
@@ -633,9 +634,9 @@ cudaError_t launch_route(const q2_0_router &r, const float *logits, int64_t stri
     LAUNCH(4);
     LAUNCH(8);
     LAUNCH(16);
-    LAUNCH(32);
 #undef LAUNCH
-    return cudaErrorInvalidValue;
+    // (kTwoExperts are 10 a lane of half a warp)
+    return launch<32, 32>(r, logits, stride, n_tokens, ids, weights, s);
 }
 
 }  // namespace q2
