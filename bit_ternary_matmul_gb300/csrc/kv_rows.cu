@@ -2,7 +2,7 @@
 // and part (resize), and pages moved to the front (compact).
 //
 // Counts and tables are a few bytes a page, and what has to be decided about them is a chain: what is given
-// back, which pages are then free, which row gets which. One cluster of blocks goes through the chain,
+// back, which pages are then free, which row gets which. (So a page that is given back may be written in the same call.) One cluster of blocks goes through the chain,
 // with the cluster's barrier between its steps, so that it is one launch and no block waits for one that may not
 // have started. The tokens that move, the bulk of the bytes, are copied by a launch of the whole GPU
 // behind it, from a list that the cluster leaves.
@@ -31,7 +31,8 @@ namespace {
 constexpr int kPerLane = 8;
 constexpr int kPart = 32 * kPerLane;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyBlocks = 4;  // of an SM
+constexpr int kCopyBlocks = 4;  // of an SM (copy_kernel; of move_kernel's, with 76 registers a thread, three are there at once, and
+                                // the fourth goes through its share behind them)
 
 struct CopyArgs {
     uint4 *k, *v;
@@ -942,6 +943,7 @@ cudaError_t compact_run(const q2_0_kv_cache &c, const q2_0_kv_rows &r, const q2_
     k.src = a.src;
     k.dst = a.dst;
     k.n_at = a.n_moves;
+    // (a fourth block of each SM runs behind the other three: see kCopyBlocks)
     return launch_behind(move_kernel, unsigned(sm_count() * kCopyBlocks), kCopyThreads, 0, false, s, a, k);
 }
 

@@ -17,10 +17,11 @@
 // the windows' (half of a run's error goes into the total as well) below 2^-38 + n_vocab 2^-58 of the total where a running
 // sum is compared with r * total.
 //
-// Measured in a CUDA graph, inputs beyond L2: 3 drafts of 1 sequence over 151936 tokens 6.4 us (1.2 MB: the bytes take 0.2, a
-// sequence of dependent reads, barriers and prefix sums the rest: 1000 tokens take 5.7), 64 sequences 16.7 (67 MB at
-// 4 TB/s; the copy rate would give 10). Inputs in L2, 4 drafts of 1 and up to 5 of 64: 7.2 and 12.3; pairs settled at every
-// addition 7.7 and 13.1, values read singly and sums in f64 19.0 and 38.7.
+// Measured in a CUDA graph, inputs beyond L2, 151936 tokens: 4 drafts of 1 sequence 8.5 us (1.2 MB: the bytes take 0.2, a
+// sequence of dependent reads, barriers and prefix sums the rest: 1000 tokens take 5.8), up to 5 of 64 16.1 (58 MB at
+// 3.6 TB/s; the copy rate would give 8.6); without the drafts' probabilities 7.8 and 14.7. Inputs in L2: 6.6 and 12.8.
+// Windows of 64 additions instead of 16, which lose more than 2^-38, take 0.6 % less; merged and settled pair by pair 1 % more.
+// Values read singly and sums in f64 took 19.0 and 38.7.
 #include <algorithm>
 #include <mutex>
 
@@ -403,7 +404,7 @@ cudaError_t launch_verify(const float *target, int64_t target_stride, const floa
     const VerifyArgs a = {target, draft,   target_stride, draft_stride, tokens, count,
                           rand,   n_draft, int(n_vocab),  accepted,     token,  err};
     // Blocks of a cluster, of 256 threads: as many as are resident together, if each has enough to read. us of 1 / 16 /
-    // 64 / 150 sequences, 3 drafts, 151936 tokens, inputs beyond L2: 1 block 24.4 / 34.2 / 48.9 / 52.9, 4 11.8 / 13.4 /
+    // 64 / 150 sequences, 3 drafts, 151936 tokens, four calls' inputs in turn (from 64 on beyond L2): 1 block 24.4 / 34.2 / 48.9 / 52.9, 4 11.8 / 13.4 /
     // 20.4 / 36.7, 8 8.1 / 9.4 / 17.3 / 35.1, 16 6.9 / 9.0 / 25.4 / 49.0; of 32003 tokens 2 7.2 / 8.5 / 8.7, 4 6.4 / 6.8 / 7.6,
     // 8 6.2 / 6.3 / 8.2; of 1000: 64 sequences 1 block 6.4, 8 7.8. (512 threads: 64 sequences 17.6, one 7.6.)
     int most = 1;

@@ -559,8 +559,8 @@ int q2_0_beam_reorder(const q2_0_kv_cache *cache, const int32_t *parent, int64_t
 typedef enum q2_0_score { Q2_0_SCORE_SOFTMAX = 0, Q2_0_SCORE_SIGMOID = 1 } q2_0_score;
 
 /*
- * q2_0_moe_route — the experts of each token, as q2_0_mul_mat_id takes them, and
- * their weights.
+ * q2_0_moe_route — the experts of each token, as q2_0_mul_mat_id takes them (up to
+ * 65535 slots a call; a prompt of more in several), and their weights.
  *   s = softmax(x) over the n_expert logits, or sigmoid(x); key = s + bias.
  *   With n_group_used < n_group the experts are n_group runs of n_expert / n_group;
  *   a group's score is the sum of its group_top (1 or 2) highest keys, and only the
@@ -574,6 +574,8 @@ typedef enum q2_0_score { Q2_0_SCORE_SOFTMAX = 0, Q2_0_SCORE_SIGMOID = 1 } q2_0_
  * A logit of -inf or NaN, or a bias of either, masks its expert: it adds nothing
  * to its group, comes after all others, by index, and has weight 0 (so that ids
  * are always n_used different experts). +inf counts as the largest finite value.
+ * (A large finite bias in a mask's place, as -1e9, makes every row take many times
+ * as long.)
  *   logits   F32, token t's row at logits + t * stride (stride >= n_expert).
  *   ids      int32 [n_tokens][n_used].   weights  F32 [n_tokens][n_used]. They must
  *            not overlap the inputs or each other.
@@ -651,7 +653,8 @@ int q2_0_draft_verify(const float *target, int64_t target_stride, const float *d
  * e.g. while attention in flight still reads the old ones, and what their rows hold
  * in the cache: q2_0_kv_fork writes no page, q2_0_kv_compact only pages that were
  * free. q2_0_kv_resize also writes pages that are given back in it: attention on old
- * rows that give pages back has to end before the call, on others it may go on.
+ * rows that give pages back has to end before the call, on others it may go on until
+ * something is appended.
  * The three arrays must not overlap one another, and a call's other arrays and its
  * workspace not those that it writes, nor the cache's pages where a call writes
  * these or the array: Q2_0_EINVAL. Rows must not lie in the cache's pages either
