@@ -655,7 +655,9 @@ int q2_0_kv_resize(const q2_0_kv_cache *cache, const q2_0_kv_rows *rows, const i
     if (!valid_cache(cache) || !valid_rows(cache, rows, rows_out) || !new_len) return Q2_0_EINVAL;
     const q2_0_kv_rows &out = rows_out ? *rows_out : *rows;
     // (the lengths themselves, in place, are read before they are written)
-    if (!(new_len == rows->len && out.len == rows->len) && !apart(new_len, rows->n_rows * 4, cache, out)) return Q2_0_EINVAL;
+    if (!(new_len == rows->len && out.len == rows->len) &&
+        (!apart(new_len, rows->n_rows * 4, cache, out) || in_cache(new_len, rows->n_rows * 4, cache)))
+        return Q2_0_EINVAL;
     const size_t need = resize_workspace_bytes(cache->n_pages, rows->n_rows);
     if (!valid_rows_workspace(workspace, workspace_bytes, need, cache, *rows, out) ||
         overlap(workspace, int64_t(need), new_len, rows->n_rows * 4))

@@ -656,9 +656,9 @@ int q2_0_draft_verify(const float *target, int64_t target_stride, const float *d
  * rows that give pages back has to end before the call, on others it may go on until
  * something is appended.
  * The three arrays must not overlap one another, and a call's other arrays and its
- * workspace not those that it writes, nor the cache's pages where a call writes
- * these or the array: Q2_0_EINVAL. Rows must not lie in the cache's pages either
- * (that is not checked). The calls below must not overlap one another on the GPU
+ * workspace not those that it writes, nor, but for the arrays of q2_0_kv_fork, the
+ * cache's pages: Q2_0_EINVAL. Rows must not lie in the cache's pages either (that is
+ * not checked). The calls below must not overlap one another on the GPU
  * where they have rows, pages or a workspace in common.
  */
 typedef struct q2_0_kv_rows {

@@ -254,6 +254,20 @@ def test_numbers_in_the_pages_that_a_call_writes_are_refused(L):
     _passes(copy, count=None)
 
 
+def test_new_lengths_in_the_cache_are_refused(L):
+    """Pages of keys and values are written by a change of lengths; the lengths themselves may be given, wherever they are."""
+    k, v, far = P, P + (1 << 18), P + (1 << 19)
+    c, r = _cache(k=k, v=v), _rows(refs=far + 4096, table=far + 8192, len=far + 12288)
+
+    def call(new):
+        return L.q2_0_kv_resize(_ref(c), _ref(r), new, None, None, 0, None)
+    for base in (k, v):
+        for p in (base, base - 12, base + 81920 - 4):
+            assert call(p) == EINVAL, p
+        for p in (base - 16, base + 81920, far + 12288):
+            _passes(call, new=p)
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     f, i = torch.zeros((2, 3, 5)), torch.zeros((2, 2), dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
