@@ -2,8 +2,8 @@
 // and part (resize), and pages moved to the front (compact).
 //
 // Counts and tables are a few bytes a page, and what has to be decided about them is a chain: what is given
-// back, which pages are then free, which row gets which. (So a page that is given back may be written in the same call.) One cluster of blocks goes through the chain,
-// with the cluster's barrier between its steps, so that it is one launch and no block waits for one that may not
+// back, which pages are then free, which row gets which. (So a page that is given back may be written in the same
+// call.) One cluster of blocks goes through the chain, with the cluster's barrier between its steps, so that it is one launch and no block waits for one that may not
 // have started. The tokens that move, the bulk of the bytes, are copied by a launch of the whole GPU
 // behind it, from a list that the cluster leaves.
 //

@@ -2,7 +2,8 @@
 // weights, for the expert products.
 //
 // A row has a warp, or half of one where it has few experts; as many warps as are resident go from row to row with
-// the next one's logits on their way (16384 rows on 4864 warps are 3.4 each, so that some have 4 and others 3). A lane holds a run of neighbouring experts in registers, so that a row is
+// the next one's logits on their way (16384 rows on 4864 warps are 3.4 each, so that some have 4 and others 3). A lane
+// holds a run of neighbouring experts in registers, so that a row is
 // read once and no block waits for another. It sorts its own keys (a network of minima and maxima, without the
 // experts) into a list in shared memory; then the best of all lanes are taken one a round, by one
 // reduction over the lists' heads and a ballot: of equal heads the lowest lane's, which are the lowest

@@ -404,7 +404,8 @@ cudaError_t launch_verify(const float *target, int64_t target_stride, const floa
     const VerifyArgs a = {target, draft,   target_stride, draft_stride, tokens, count,
                           rand,   n_draft, int(n_vocab),  accepted,     token,  err};
     // Blocks of a cluster, of 256 threads: as many as are resident together, if each has enough to read. us of 1 / 16 /
-    // 64 / 150 sequences, 3 drafts, 151936 tokens, four calls' inputs in turn (from 64 on beyond L2): 1 block 24.4 / 34.2 / 48.9 / 52.9, 4 11.8 / 13.4 /
+    // 64 / 150 sequences, 3 drafts, 151936 tokens, four calls' inputs in turn (from 64 on beyond L2): 1 block
+    // 24.4 / 34.2 / 48.9 / 52.9, 4 11.8 / 13.4 /
     // 20.4 / 36.7, 8 8.1 / 9.4 / 17.3 / 35.1, 16 6.9 / 9.0 / 25.4 / 49.0; of 32003 tokens 2 7.2 / 8.5 / 8.7, 4 6.4 / 6.8 / 7.6,
     // 8 6.2 / 6.3 / 8.2; of 1000: 64 sequences 1 block 6.4, 8 7.8. (512 threads: 64 sequences 17.6, one 7.6.)
     int most = 1;
